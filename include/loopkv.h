@@ -371,6 +371,181 @@ loopkv_status loopkv_vq_encode(const loopkv_vq_desc* desc, const int32_t* h_pos,
                                const uint16_t* d_x, const float* d_cb, uint8_t* d_idx,
                                void* stream);
 
+/* ---- Paged cells --------------------------------------------------------
+ * The cache of cells whose units are not given a region of fixed capacity:
+ * tokens live in pages of `page_size` tokens, taken from a pool when a
+ * request grows and given back when it ends.  One block table serves every
+ * cell, because all cells of a request hold the same tokens; a SHARE cell
+ * owns no pages and reads the final loop's.  Lengths, tables, the free list
+ * and the slot maps live on the device, so a whole serving step can be
+ * captured into a CUDA graph and replayed any number of times.
+ *
+ * Pool.  k, v: [n_cells][n_pages][n_kv_heads][page_size][head_dim], bf16,
+ * fp16, or one byte per value (LOOPKV_PAGE_Q8).  Q8 adds meta: fp32
+ * [n_cells][n_pages][n_kv_heads][page_size][4] = {key scale, key zero point,
+ * value scale, value zero point} of each token and head: x ~ scale * code +
+ * zero with scale = fl(fl(max - min) / 255), zero = min (a zero min is stored
+ * as +0), code = rne(fl(fl(x - min) / scale)) clamped to 0..255, scale 0
+ * giving codes 0: the quantizer of the 4-bit cells with 255 steps, grouped
+ * per token for keys too, since pages take tokens one at a time and in any
+ * order.  Inputs of a Q8 append are finite.
+ * Tables.  d_table: int32 [batch][max_pages]; token t of request b is in
+ * page d_table[b][t / page_size] at offset t % page_size.  Entries behind a
+ * request's last page mean nothing and are never read.  slot = page *
+ * page_size + offset.
+ * Limits.  batch <= LOOPKV_MAX_PAGED_BATCH; max_pages * page_size <=
+ * LOOPKV_MAX_PAGED_TOKENS; n_pages * page_size < 2^31; the pool's token rows
+ * n_cells * n_pages * n_kv_heads * page_size < 2^32 - 1.
+ *
+ * Status.  Every call takes a device word d_status (NULL: none) into which
+ * its kernel ORs LOOPKV_PAGE_* bits where the device data ask for something
+ * that cannot be done; what each call does then is written with it.  Nothing
+ * outside the given arrays is read or written whatever the device data hold.
+ * The arrays of one call must not overlap, except where a call says so. */
+typedef enum {
+  LOOPKV_PAGE_BF16 = 0,
+  LOOPKV_PAGE_F16 = 1,
+  LOOPKV_PAGE_Q8 = 2
+} loopkv_page_format;
+
+#define LOOPKV_MAX_PAGED_BATCH 4096
+#define LOOPKV_MAX_PAGED_TOKENS (1 << 22)
+/* Largest query group (query heads per KV head) of loopkv_paged_decode. */
+#define LOOPKV_MAX_PAGED_GROUP 16
+
+#define LOOPKV_PAGE_BAD_LENGTH 1u /* a length, token count or free count out of range */
+#define LOOPKV_PAGE_NO_TABLE 2u   /* a request would outgrow its table row */
+#define LOOPKV_PAGE_NO_ROWS 4u    /* a request's tokens do not fit the slot map */
+#define LOOPKV_PAGE_NO_PAGES 8u   /* the free list is too short (or too full to push to) */
+#define LOOPKV_PAGE_BAD_PAGE 16u  /* a table or free-list entry outside the pool */
+#define LOOPKV_PAGE_BAD_SLOT 32u  /* a slot outside the pool */
+
+/* Room for new tokens: block tables and slot map from request lengths.  For
+ * request b < batch, holding d_len[b] tokens and bringing d_new[b]:
+ *     d_starts[b] = sum of d_new[i], i < b (negative ones count 0), so that
+ *                   request b's new tokens are rows d_starts[b] ..; d_starts
+ *                   has batch + 1 entries, saturating at 2^31 - 1;
+ *     pages it lacks, ceil((len + new) / page_size) - ceil(len / page_size),
+ *                   are popped from the free list's end in (b, page) order and
+ *                   entered in its table row;
+ *     d_slots[d_starts[b] + i] = the slot of its token len + i;
+ *     d_newest[b] = the slot of its last new token, -1 if it has none (for
+ *                   steps that keep request b's vectors in row b);
+ *     d_len_out[b] = len + new;  *d_free_count_out = *d_free_count - pages.
+ * Rows of d_slots [n_rows] that no token has get -1.  A request is refused
+ * - its length stays, its rows get -1, it takes no page - when its length or
+ * count is negative (BAD_LENGTH), when it would outgrow max_pages (NO_TABLE)
+ * or its rows end behind n_rows (NO_ROWS), and, needing pages, when they and
+ * those of the requests before it (refused ones not counted but for this
+ * reason) are more than the free list has (NO_PAGES).  A page id outside
+ * 0 .. n_pages-1 gives slots -1 (BAD_PAGE).  d_free: int32 [n_pages], of which
+ * the first *d_free_count are free pages.  d_len_out may be d_len and
+ * d_free_count_out may be d_free_count.  d_slots may be NULL (its rows are
+ * then only counted), and so may d_newest [batch].
+ * Errors (nothing launched): LOOPKV_ERR_INVALID_ARG, LOOPKV_ERR_CUDA. */
+loopkv_status loopkv_page_map(int32_t batch, int32_t page_size, int32_t max_pages, int32_t n_pages,
+                              int32_t n_rows, const int32_t* d_len, const int32_t* d_new,
+                              int32_t* d_table, const int32_t* d_free, const int32_t* d_free_count,
+                              int32_t* d_slots, int32_t* d_starts, int32_t* d_newest,
+                              int32_t* d_len_out, int32_t* d_free_count_out, uint32_t* d_status,
+                              void* stream);
+
+/* Give pages back: request b is cut from d_len[b] to d_new_len[b] tokens (0:
+ * it ended; its own length: nothing happens), and its pages
+ * ceil(new / page_size) .. ceil(len / page_size) - 1 are pushed to the free
+ * list's end in (b, page) order; d_len_out[b] = new, *d_free_count_out grows
+ * by the pages.  Table entries stay as they are.  Pages are pushed once per
+ * table entry: a page that two requests' tables hold is the caller's to count.
+ * A request is refused (nothing pushed, its length stays) when new < 0, new >
+ * len or len > max_pages * page_size (BAD_LENGTH), or when the free list
+ * would outgrow n_pages with it (NO_PAGES).  A table entry outside the pool
+ * is pushed as -1 (BAD_PAGE; loopkv_page_map gives no slot on it).  d_len_out
+ * may be d_len or d_new_len, and d_free_count_out may be d_free_count.
+ * Errors (nothing launched): LOOPKV_ERR_INVALID_ARG, LOOPKV_ERR_CUDA. */
+loopkv_status loopkv_page_release(int32_t batch, int32_t page_size, int32_t max_pages,
+                                  int32_t n_pages, const int32_t* d_len, const int32_t* d_new_len,
+                                  const int32_t* d_table, int32_t* d_free,
+                                  const int32_t* d_free_count, int32_t* d_len_out,
+                                  int32_t* d_free_count_out, uint32_t* d_status, void* stream);
+
+typedef struct {
+  int32_t n_cells;     /* cells of the pool */
+  int32_t n_pages;     /* pages of each cell */
+  int32_t page_size;   /* tokens per page, 1 .. 1024 */
+  int32_t n_kv_heads;  /* 1 .. 65536 */
+  int32_t head_dim;    /* 64 or 128 */
+  int32_t format;      /* loopkv_page_format */
+  void* k;             /* device, 16-byte aligned */
+  void* v;
+  float* meta;         /* LOOPKV_PAGE_Q8 only, else NULL */
+} loopkv_page_pool;
+
+/* Rows of head vectors: the vector of (cell, row, head) starts at element
+ * cell * cell_stride + row * row_stride + head * head_stride of data; its
+ * head_dim elements are contiguous.  Strides are in elements, not negative,
+ * and multiples of 8; data is 16-byte aligned.  Elements are bf16 (fp16 for
+ * LOOPKV_PAGE_F16). */
+typedef struct {
+  const void* data;
+  int64_t cell_stride, row_stride, head_stride;
+} loopkv_rows;
+
+/* Write new tokens into their slots: for the i-th listed cell c = h_cells[i]
+ * (host, distinct pool cells; -1: the i-th input belongs to a cell that
+ * stores nothing and is skipped), row r < n_rows and head h, vectors (i, r, h)
+ * of k and v go to slot d_slots[r] of cell c, as they are or quantized (Q8).
+ * Rows with slot -1 are skipped, slots below -1 or outside the pool too
+ * (BAD_SLOT).  Slots of one call are distinct (two rows of one slot leave a
+ * mixture of both).
+ * Errors (nothing launched): LOOPKV_ERR_INVALID_ARG, LOOPKV_ERR_UNSUPPORTED
+ * (more than 2^31 blocks of work), LOOPKV_ERR_CUDA. */
+loopkv_status loopkv_paged_append(const loopkv_page_pool* pool, const int32_t* h_cells,
+                                  int32_t n_cells, int32_t n_rows, const int32_t* d_slots,
+                                  const loopkv_rows* k, const loopkv_rows* v, uint32_t* d_status,
+                                  void* stream);
+
+typedef struct {
+  int32_t batch;           /* requests, 1 .. LOOPKV_MAX_PAGED_BATCH */
+  int32_t max_pages;       /* table width */
+  int32_t q_per_kv;        /* query heads per KV head, 1 .. LOOPKV_MAX_PAGED_GROUP */
+  float sm_scale;          /* <= 0 means 1/sqrt(head_dim) */
+} loopkv_paged_desc;
+
+/* Device bytes of workspace that a loopkv_paged_decode of these sizes needs.
+ * It holds nothing between calls and needs no initialisation; calls that may
+ * run at the same time need one each. */
+loopkv_status loopkv_paged_workspace(const loopkv_page_pool* pool, const loopkv_paged_desc* desc,
+                                     size_t* bytes);
+
+/* Attention of one new token per request over its pages.  For the i-th listed
+ * cell c = h_cells[i] (host, pool cells; a cell may be listed more than once:
+ * loops that share it), request b, KV head h and query r < g = q_per_kv, with
+ * the query of query head h * g + r in row b of q, over the tokens t <
+ * d_len[b] of the pages: scores sm_scale * <q, k_t>, softmax, and
+ *     d_out [n_cells][batch][n_kv_heads * g][head_dim] = sum_t p_t v_t
+ * in q's type (bf16; fp16 for LOOPKV_PAGE_F16), and, unless d_lse is NULL,
+ *     d_lse fp32 [n_cells][batch][n_kv_heads * g], the natural log of
+ *     sum_t exp(score_t).
+ * Where h_current (host [n_cells], NULL: nowhere) is not 0, the last token,
+ * t = d_len[b] - 1, is read from row b of cur_k and cur_v ((i, b, h) vectors)
+ * instead of its page: a SHARE cell, whose current token no page holds.  A
+ * request without tokens, or without a score above -infinity, gives zeros and
+ * lse -infinity.  Lengths below 0 or above max_pages * page_size count as 0
+ * (BAD_LENGTH); tokens on a page outside the pool are left out (BAD_PAGE).
+ * What pages hold behind a request's length has no influence.  Softmax weights
+ * are kept to about 16 bits (bf16 pairs) where they meet the values, sums are
+ * fp32; the order of all sums is fixed by the sizes and lengths.
+ * Errors (nothing launched): LOOPKV_ERR_INVALID_ARG (null or misaligned
+ * pointers, sizes, a workspace below loopkv_paged_workspace's bytes),
+ * LOOPKV_ERR_CUDA. */
+loopkv_status loopkv_paged_decode(const loopkv_page_pool* pool, const loopkv_paged_desc* desc,
+                                  const int32_t* h_cells, const uint8_t* h_current, int32_t n_cells,
+                                  const int32_t* d_table, const int32_t* d_len,
+                                  const loopkv_rows* q, const loopkv_rows* cur_k,
+                                  const loopkv_rows* cur_v, void* d_out, float* d_lse,
+                                  void* d_work, size_t work_bytes, uint32_t* d_status,
+                                  void* stream);
+
 #ifdef __cplusplus
 }
 #endif

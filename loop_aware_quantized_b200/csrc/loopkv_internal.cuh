@@ -144,6 +144,33 @@ struct DecodeParams {
   float score_scale;           // sm_scale * log2(e): scores are kept in log2 units
 };
 
+// ---------------------------------------------------------- paged cells
+
+constexpr int kMaxPageSize = 1024;
+
+// Division by the page size without a divide: for 0 <= n < 2^31 and
+// s = ceil(log2 size), mul = ceil(2^(31+s) / size) exceeds the true ratio by
+// less than 1, so (n * mul) >> (31 + s) = floor(n / size) (the error n * (mul
+// - ratio) / 2^(31+s) stays below 2^-s <= 1 / size).
+struct PageDiv {
+  uint32_t mul;   // 2^31 .. 2^32 - 1
+  int32_t shift;  // 31 + s
+  int32_t size;
+  PageDiv() = default;
+  explicit PageDiv(int d) : size(d) {
+    int s = 0;
+    while ((1 << s) < d) ++s;
+    shift = 31 + s;
+    mul = (uint32_t)(((1ull << shift) + (uint64_t)d - 1) / (uint64_t)d);
+  }
+  __host__ __device__ int page(int n) const { return (int)(((uint64_t)(uint32_t)n * mul) >> shift); }
+  __host__ __device__ int pages(int n) const { return page(n + size - 1); }  // pages of n tokens
+};
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool pool_ok(const loopkv_page_pool* p);  // paged_append.cu: argument checks of the paged calls
+bool rows_ok(const loopkv_rows* r);
+
 // Launchers (decode.cu / append.cu).  Return cudaGetLastError() as int.
 // res2: the cells are all RES2 (their own kernel); else none is.  cells.out[i]
 // is cell i's index in the caller's list (its slot of the inputs / outputs).

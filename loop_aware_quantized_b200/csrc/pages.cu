@@ -1,0 +1,418 @@
+// Block tables and slot maps from request lengths, and pages given back, for
+// sm_100a: the bookkeeping of the paged cells on the device.
+//
+// Both calls are a prefix sum over the requests followed by a flat expansion:
+//   page_map      rows  r of the slot map: request b with start_b <= r,
+//                 position len_b + r - start_b, its page from the table (the
+//                 partly filled one) or from the free list (a new one; every
+//                 new page holds one of the new tokens at offset 0, and the
+//                 thread of that row enters it in the table);
+//   page_release  pages i of the free list's new end: request b with
+//                 start_b <= i, its table entry.
+// One thread-block cluster does a whole call.  Every CTA reads the lengths
+// and does the (short) prefix sum for itself, so nothing but the cluster
+// barrier at the end joins them: behind it no CTA reads the lengths or the
+// free count any more and the first one stores the new ones, which is what
+// lets them be updated in place by one launch, and the call be captured and
+// replayed.  What bounds it: the launch and two dependent memory round trips
+// (lengths, then free list or table) for a decode step, the writes of a
+// cluster's SMs for long prompts.
+
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "loopkv_internal.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace loopkv {
+namespace {
+
+constexpr int kPageThreads = 1024;
+constexpr int kPageWarps = kPageThreads / 32;
+constexpr int kPerThread = LOOPKV_MAX_PAGED_BATCH / kPageThreads;  // requests per thread at most
+constexpr int kChunk = 512;     // rows a warp expands with one search
+constexpr int kClusterRows = 4096;  // rows one CTA takes before a cluster of 8 does
+constexpr long long kSatRows = 0x7fffffffLL;
+
+// Exclusive prefix sum over the block's threads; *total gets the sum.
+__device__ __forceinline__ long long block_scan(long long x, long long* warp_sums, long long* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long inc = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  __syncthreads();  // the last scan's readers are done
+  if (lane == 31) warp_sums[warp] = inc;
+  __syncthreads();
+  if (warp == 0) {
+    long long s = warp_sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += y;
+    }
+    warp_sums[lane] = s;
+  }
+  __syncthreads();
+  *total = warp_sums[kPageWarps - 1];
+  return (warp == 0 ? 0 : warp_sums[warp - 1]) + inc - x;
+}
+
+// Largest b in [lo, hi] with start[b] <= r (start ascends, start[lo] <= r):
+// among requests without rows, which share a start, the one that has row r.
+__device__ __forceinline__ int find_request(const int* start, int lo, int hi, int r) {
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (start[mid] <= r) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+struct PageParams {
+  const int32_t* len;
+  const int32_t* count;        // new tokens (map), new lengths (release)
+  int32_t* table;
+  int32_t* free;
+  const int32_t* free_count;
+  int32_t* slots;
+  int32_t* starts;
+  int32_t* newest;
+  int32_t* len_out;
+  int32_t* free_count_out;
+  uint32_t* status;
+  int32_t batch, max_pages, n_pages, n_rows;
+  PageDiv div;
+};
+
+// Per request, in shared memory: start[batch + 1], then two values the
+// expansion needs (map: length or -1, index into the free list of its first
+// new page; release: first page given back, unused).
+struct Shared {
+  int* start;
+  int* a;
+  int* b;
+};
+
+__device__ __forceinline__ Shared shared_arrays(int* mem, int batch) {
+  return {mem, mem + batch + 1, mem + 2 * batch + 1};
+}
+
+__global__ void __launch_bounds__(kPageThreads) page_map_kernel(const __grid_constant__ PageParams p) {
+  extern __shared__ int mem[];
+  __shared__ long long warp_sums[32];
+  const Shared sh = shared_arrays(mem, p.batch);
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
+  const int tid = threadIdx.x, per = (p.batch + kPageThreads - 1) / kPageThreads;
+  uint32_t status = 0;
+
+  int len[kPerThread], add[kPerThread];
+  long long rows = 0;
+#pragma unroll
+  for (int k = 0; k < kPerThread; ++k) {
+    const int b = tid * per + k;
+    const bool in = k < per && b < p.batch;
+    len[k] = in ? p.len[b] : 0;
+    add[k] = in ? p.count[b] : 0;
+    rows += add[k] > 0 ? add[k] : 0;
+  }
+  int free_count = *p.free_count;
+  if (free_count < 0 || free_count > p.n_pages) {
+    status |= LOOPKV_PAGE_BAD_LENGTH;
+    free_count = 0;
+  }
+  long long all_rows, all_need;
+  long long start = block_scan(rows, warp_sums, &all_rows);
+  const long long capacity = (long long)p.max_pages * p.div.size;
+  int need[kPerThread];
+  long long sum = 0;
+#pragma unroll
+  for (int k = 0; k < kPerThread; ++k) {
+    const int b = tid * per + k;
+    need[k] = 0;
+    if (k >= per || b >= p.batch) continue;
+    const long long n = add[k] > 0 ? add[k] : 0;
+    uint32_t bad = 0;
+    if (len[k] < 0 || add[k] < 0) bad = LOOPKV_PAGE_BAD_LENGTH;
+    else if ((long long)len[k] + n > capacity) bad = LOOPKV_PAGE_NO_TABLE;
+    else if (start + n > p.n_rows) bad = LOOPKV_PAGE_NO_ROWS;
+    sh.start[b] = (int)(start < kSatRows ? start : kSatRows);
+    start += n;
+    if (bad) {
+      status |= bad;
+      add[k] = -1;  // refused
+    } else {
+      need[k] = p.div.pages(len[k] + (int)n) - p.div.pages(len[k]);
+      sum += need[k];
+    }
+  }
+  long long before = block_scan(sum, warp_sums, &all_need);
+  const int total = (int)(all_rows < kSatRows ? all_rows : kSatRows);
+  long long taken = 0;  // pages of the admitted requests so far
+#pragma unroll
+  for (int k = 0; k < kPerThread; ++k) {
+    const int b = tid * per + k;
+    if (k >= per || b >= p.batch) continue;
+    if (need[k] > 0 && before + need[k] > free_count) {
+      status |= LOOPKV_PAGE_NO_PAGES;
+      add[k] = -1;
+    } else if (need[k] > 0) {
+      taken = before + need[k];  // admitted requests that need pages are a prefix
+    }
+    sh.a[b] = add[k] < 0 ? -1 : len[k];
+    sh.b[b] = (int)(free_count - 1 - before);
+    before += need[k];
+  }
+  if (tid == 0) sh.start[p.batch] = total;
+  __syncthreads();
+
+  // Rows, in chunks of kChunk to a warp.
+  const int lane = tid & 31;
+  const long long step = (long long)ranks * kPageWarps * kChunk;
+  for (long long r0 = ((long long)(tid >> 5) * ranks + rank) * kChunk; r0 < p.n_rows; r0 += step) {
+    const int r1 = (int)(r0 + kChunk < p.n_rows ? r0 + kChunk : p.n_rows);
+    const int lo = find_request(sh.start, 0, p.batch - 1, (int)r0);
+    const int hi = find_request(sh.start, lo, p.batch - 1, r1 - 1);
+    for (int r = (int)r0 + lane; r < r1; r += 32) {
+      int slot = -1;
+      if (r < total) {
+        const int b = find_request(sh.start, lo, hi, r);
+        const int n = sh.a[b];
+        if (n >= 0) {
+          const int pos = n + (r - sh.start[b]);
+          const int held = p.div.pages(n), j = p.div.page(pos), off = pos - j * p.div.size;
+          int32_t* entry = p.table + (size_t)b * p.max_pages + j;
+          const int page = j < held ? *entry : p.free[sh.b[b] - (j - held)];
+          const bool good = page >= 0 && page < p.n_pages;
+          if (j >= held && off == 0) *entry = good ? page : -1;
+          if (good) slot = page * p.div.size + off;
+          else status |= LOOPKV_PAGE_BAD_PAGE;
+          if (p.newest && r + 1 == sh.start[b + 1]) p.newest[b] = slot;
+        }
+      }
+      if (p.slots) p.slots[r] = slot;
+    }
+  }
+  if (rank == 0) {
+    for (int b = tid; b <= p.batch; b += kPageThreads) {
+      p.starts[b] = sh.start[b];
+      // the other requests' newest slots come from the threads of their last rows
+      if (p.newest && b < p.batch && (sh.a[b] < 0 || sh.start[b] == sh.start[b + 1])) p.newest[b] = -1;
+    }
+  }
+  if (status && p.status) atomicOr(p.status, status);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const long long y = __shfl_xor_sync(0xffffffffu, taken, o);
+    taken = y > taken ? y : taken;
+  }
+  if (lane == 0) warp_sums[tid >> 5] = taken;
+  cluster.sync();  // every CTA has read the lengths and the free count
+  if (rank != 0) return;
+#pragma unroll
+  for (int k = 0; k < kPerThread; ++k) {
+    const int b = tid * per + k;
+    if (k < per && b < p.batch) p.len_out[b] = add[k] > 0 ? len[k] + add[k] : len[k];
+  }
+  if (tid == 0) {
+    long long most = 0;
+    for (int w = 0; w < kPageWarps; ++w) most = warp_sums[w] > most ? warp_sums[w] : most;
+    *p.free_count_out = free_count - (int)most;
+  }
+}
+
+__global__ void __launch_bounds__(kPageThreads)
+page_release_kernel(const __grid_constant__ PageParams p) {
+  extern __shared__ int mem[];
+  __shared__ long long warp_sums[32];
+  const Shared sh = shared_arrays(mem, p.batch);
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
+  const int tid = threadIdx.x, per = (p.batch + kPageThreads - 1) / kPageThreads;
+  uint32_t status = 0;
+
+  int len[kPerThread], cut[kPerThread], gone[kPerThread];
+  int free_count = *p.free_count;
+  if (free_count < 0 || free_count > p.n_pages) {
+    status |= LOOPKV_PAGE_BAD_LENGTH;
+    free_count = p.n_pages;  // nothing can be pushed
+  }
+  const long long capacity = (long long)p.max_pages * p.div.size;
+  long long sum = 0;
+#pragma unroll
+  for (int k = 0; k < kPerThread; ++k) {
+    const int b = tid * per + k;
+    gone[k] = 0;
+    if (k >= per || b >= p.batch) continue;
+    len[k] = p.len[b];
+    cut[k] = p.count[b];
+    if (cut[k] < 0 || cut[k] > len[k] || len[k] > capacity) {
+      status |= LOOPKV_PAGE_BAD_LENGTH;
+      cut[k] = len[k];
+    } else {
+      gone[k] = p.div.pages(len[k]) - p.div.pages(cut[k]);
+      sum += gone[k];
+    }
+  }
+  long long all;
+  long long before = block_scan(sum, warp_sums, &all);
+  const long long room = p.n_pages - free_count;
+  long long pushed = 0;
+#pragma unroll
+  for (int k = 0; k < kPerThread; ++k) {
+    const int b = tid * per + k;
+    if (k >= per || b >= p.batch) continue;
+    // starts of refused requests lie at or behind `room`, where no push is made
+    sh.start[b] = (int)(before < room ? before : room);
+    sh.a[b] = gone[k] > 0 ? p.div.pages(cut[k]) : 0;
+    before += gone[k];
+    if (gone[k] > 0 && before > room) {
+      status |= LOOPKV_PAGE_NO_PAGES;
+      cut[k] = len[k];
+    } else if (gone[k] > 0) {
+      pushed = before;
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const long long y = __shfl_xor_sync(0xffffffffu, pushed, o);
+    pushed = y > pushed ? y : pushed;
+  }
+  __syncthreads();  // the scan's readers of warp_sums are done
+  const int lane = tid & 31;
+  if (lane == 0) warp_sums[tid >> 5] = pushed;
+  __syncthreads();
+  long long most = 0;
+  for (int w = 0; w < kPageWarps; ++w) most = warp_sums[w] > most ? warp_sums[w] : most;
+
+  const int total = (int)most;  // pages pushed: those of the admitted requests, a prefix
+  const long long step = (long long)ranks * kPageWarps * kChunk;
+  for (long long i0 = ((long long)(tid >> 5) * ranks + rank) * kChunk; i0 < total; i0 += step) {
+    const int i1 = (int)(i0 + kChunk < total ? i0 + kChunk : total);
+    const int lo = find_request(sh.start, 0, p.batch - 1, (int)i0);
+    const int hi = find_request(sh.start, lo, p.batch - 1, i1 - 1);
+    for (int i = (int)i0 + lane; i < i1; i += 32) {
+      const int b = find_request(sh.start, lo, hi, i);
+      int page = p.table[(size_t)b * p.max_pages + sh.a[b] + (i - sh.start[b])];
+      if (page < 0 || page >= p.n_pages) {
+        status |= LOOPKV_PAGE_BAD_PAGE;
+        page = -1;
+      }
+      p.free[free_count + i] = page;
+    }
+  }
+  if (status && p.status) atomicOr(p.status, status);
+  cluster.sync();  // every CTA has read the lengths and the free count
+  if (rank != 0) return;
+#pragma unroll
+  for (int k = 0; k < kPerThread; ++k) {
+    const int b = tid * per + k;
+    if (k < per && b < p.batch) p.len_out[b] = cut[k];
+  }
+  if (tid == 0) *p.free_count_out = free_count + total;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+bool page_args_ok(int32_t batch, int32_t page_size, int32_t max_pages, int32_t n_pages) {
+  return batch >= 1 && batch <= LOOPKV_MAX_PAGED_BATCH && page_size >= 1 &&
+         page_size <= kMaxPageSize && max_pages >= 1 &&
+         (long long)max_pages * page_size <= LOOPKV_MAX_PAGED_TOKENS && n_pages >= 1 &&
+         (long long)n_pages * page_size < (1LL << 31);
+}
+
+// work: rows (map) or pages (release) the call may have to expand, at most.
+template <typename Kernel>
+loopkv_status launch_pages(Kernel kernel, const PageParams& p, long long work, void* stream) {
+  const size_t smem = sizeof(int) * (3 * (size_t)p.batch + 1);
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return LOOPKV_ERR_CUDA;
+  const unsigned ctas = work <= kClusterRows ? 1 : 8;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas, 1, 1);
+  cfg.blockDim = dim3(kPageThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? LOOPKV_OK : LOOPKV_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace loopkv
+
+using namespace loopkv;
+
+extern "C" loopkv_status loopkv_page_map(int32_t batch, int32_t page_size, int32_t max_pages,
+                                         int32_t n_pages, int32_t n_rows, const int32_t* d_len,
+                                         const int32_t* d_new, int32_t* d_table,
+                                         const int32_t* d_free, const int32_t* d_free_count,
+                                         int32_t* d_slots, int32_t* d_starts, int32_t* d_newest,
+                                         int32_t* d_len_out, int32_t* d_free_count_out,
+                                         uint32_t* d_status, void* stream) {
+  if (!page_args_ok(batch, page_size, max_pages, n_pages) || n_rows < 0 || n_rows > (1 << 30))
+    return LOOPKV_ERR_INVALID_ARG;
+  const void* ptrs[8] = {d_len, d_new, d_table, d_free, d_free_count, d_starts, d_len_out,
+                         d_free_count_out};
+  for (const void* ptr : ptrs)
+    if (ptr == nullptr || !aligned4(ptr)) return LOOPKV_ERR_INVALID_ARG;
+  if (!aligned4(d_slots) || !aligned4(d_newest) || !aligned4(d_status)) return LOOPKV_ERR_INVALID_ARG;
+  PageParams p{};
+  p.len = d_len;
+  p.count = d_new;
+  p.table = d_table;
+  p.free = const_cast<int32_t*>(d_free);
+  p.free_count = d_free_count;
+  p.slots = d_slots;
+  p.starts = d_starts;
+  p.newest = d_newest;
+  p.len_out = d_len_out;
+  p.free_count_out = d_free_count_out;
+  p.status = d_status;
+  p.batch = batch;
+  p.max_pages = max_pages;
+  p.n_pages = n_pages;
+  p.n_rows = n_rows;
+  p.div = PageDiv(page_size);
+  return launch_pages(page_map_kernel, p, n_rows, stream);
+}
+
+extern "C" loopkv_status loopkv_page_release(int32_t batch, int32_t page_size, int32_t max_pages,
+                                             int32_t n_pages, const int32_t* d_len,
+                                             const int32_t* d_new_len, const int32_t* d_table,
+                                             int32_t* d_free, const int32_t* d_free_count,
+                                             int32_t* d_len_out, int32_t* d_free_count_out,
+                                             uint32_t* d_status, void* stream) {
+  if (!page_args_ok(batch, page_size, max_pages, n_pages)) return LOOPKV_ERR_INVALID_ARG;
+  const void* ptrs[7] = {d_len, d_new_len, d_table, d_free, d_free_count, d_len_out,
+                         d_free_count_out};
+  for (const void* ptr : ptrs)
+    if (ptr == nullptr || !aligned4(ptr)) return LOOPKV_ERR_INVALID_ARG;
+  if (!aligned4(d_status)) return LOOPKV_ERR_INVALID_ARG;
+  PageParams p{};
+  p.len = d_len;
+  p.count = d_new_len;
+  p.table = const_cast<int32_t*>(d_table);
+  p.free = d_free;
+  p.free_count = d_free_count;
+  p.len_out = d_len_out;
+  p.free_count_out = d_free_count_out;
+  p.status = d_status;
+  p.batch = batch;
+  p.max_pages = max_pages;
+  p.n_pages = n_pages;
+  p.div = PageDiv(page_size);
+  const long long most = std::min<long long>((long long)batch * max_pages, n_pages);
+  return launch_pages(page_release_kernel, p, most, stream);
+}

@@ -45,8 +45,6 @@ constexpr uint32_t kMagic = 0x4C4B5631u;  // "LKV1"
 constexpr int kMaxCells = 4096;
 constexpr int kMaxCapacity = 1 << 20;
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 loopkv_status validate_desc(const loopkv_plan_desc* d) {
   if (d == nullptr || d->capacity == nullptr || d->kinds == nullptr) return LOOPKV_ERR_INVALID_ARG;
   if (d->n_loops < 1 || d->n_layers < 1 || d->n_kv_heads < 1) return LOOPKV_ERR_PLAN;

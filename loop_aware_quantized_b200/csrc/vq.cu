@@ -492,8 +492,6 @@ int launch_vq_t(const VqParams& p, long long units, cudaStream_t stream) {
   return (int)cudaLaunchKernelEx(&cfg, vq_decode_kernel<D>, p);
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 bool vq_desc_ok(const loopkv_vq_desc* d) {
   return d != nullptr && d->n_loops >= 1 && d->n_loops <= 8 && d->n_layers >= 1 &&
          d->n_kv_heads >= 1 && d->n_kv_heads <= (1 << 16) &&

@@ -21,6 +21,12 @@ LIB_PATH = os.path.join(_HERE, "libloopkv.so")
 LOOPKV_Q4, LOOPKV_Q2, LOOPKV_SHARE, LOOPKV_BF16, LOOPKV_RES2 = 0, 1, 2, 3, 4
 LOOPKV_MAX_CELLS_PER_CALL = 256
 LOOPKV_MAX_BATCH = 256
+LOOPKV_PAGE_BF16, LOOPKV_PAGE_F16, LOOPKV_PAGE_Q8 = 0, 1, 2
+LOOPKV_MAX_PAGED_BATCH = 4096
+LOOPKV_MAX_PAGED_TOKENS = 1 << 22
+LOOPKV_MAX_PAGED_GROUP = 16
+LOOPKV_PAGE_BAD_LENGTH, LOOPKV_PAGE_NO_TABLE, LOOPKV_PAGE_NO_ROWS = 1, 2, 4
+LOOPKV_PAGE_NO_PAGES, LOOPKV_PAGE_BAD_PAGE, LOOPKV_PAGE_BAD_SLOT = 8, 16, 32
 
 STATUS = {
     0: "LOOPKV_OK",
@@ -84,6 +90,38 @@ class loopkv_vq_desc(ctypes.Structure):
     ]
 
 
+class loopkv_page_pool(ctypes.Structure):
+    _fields_ = [
+        ("n_cells", ctypes.c_int32),
+        ("n_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("n_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("format", ctypes.c_int32),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("meta", ctypes.c_void_p),
+    ]
+
+
+class loopkv_rows(ctypes.Structure):
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("cell_stride", ctypes.c_int64),
+        ("row_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+    ]
+
+
+class loopkv_paged_desc(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("q_per_kv", ctypes.c_int32),
+        ("sm_scale", ctypes.c_float),
+    ]
+
+
 class loopkv_sizes(ctypes.Structure):
     _fields_ = [("table_bytes", ctypes.c_size_t), ("cache_bytes", ctypes.c_size_t)]
 
@@ -115,6 +153,12 @@ def _load():
         "loopkv_vq_decode": (st, [ctypes.POINTER(loopkv_vq_desc), I32, P, P, P, P, P, P, P, P,
                                   P]),
         "loopkv_vq_encode": (st, [ctypes.POINTER(loopkv_vq_desc), P, I32, P, P, P, P]),
+        "loopkv_page_map": (st, [I32] * 5 + [P] * 12),
+        "loopkv_page_release": (st, [I32] * 4 + [P] * 9),
+        "loopkv_paged_append": (st, [P, P, I32, I32, P, P, P, P, P]),
+        "loopkv_paged_workspace": (st, [P, P, ctypes.POINTER(ctypes.c_size_t)]),
+        "loopkv_paged_decode": (st, [P, P, P, P, I32, P, P, P, P, P, P, P, P, ctypes.c_size_t, P,
+                                     P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -170,6 +214,43 @@ def loopkv_vq_decode(desc, loop, h_len, d_idx_k, d_idx_v, d_cb_k, d_cb_v, d_q, d
 def loopkv_vq_encode(desc, h_pos, n_new, d_x, d_cb, d_idx, stream):
     ref = None if desc is None else ctypes.byref(desc)
     return _lib.loopkv_vq_encode(ref, h_pos, n_new, d_x, d_cb, d_idx, stream)
+
+
+def loopkv_page_map(batch, page_size, max_pages, n_pages, n_rows, d_len, d_new, d_table, d_free,
+                    d_free_count, d_slots, d_starts, d_newest, d_len_out, d_free_count_out, d_status,
+                    stream):
+    return _lib.loopkv_page_map(batch, page_size, max_pages, n_pages, n_rows, d_len, d_new,
+                                d_table, d_free, d_free_count, d_slots, d_starts, d_newest,
+                                d_len_out, d_free_count_out, d_status, stream)
+
+
+def loopkv_page_release(batch, page_size, max_pages, n_pages, d_len, d_new_len, d_table, d_free,
+                        d_free_count, d_len_out, d_free_count_out, d_status, stream):
+    return _lib.loopkv_page_release(batch, page_size, max_pages, n_pages, d_len, d_new_len,
+                                    d_table, d_free, d_free_count, d_len_out, d_free_count_out,
+                                    d_status, stream)
+
+
+def _ref(struct):
+    return None if struct is None else ctypes.addressof(struct)
+
+
+def loopkv_paged_append(pool, h_cells, n_cells, n_rows, d_slots, k, v, d_status, stream):
+    return _lib.loopkv_paged_append(_ref(pool), h_cells, n_cells, n_rows, d_slots, _ref(k),
+                                    _ref(v), d_status, stream)
+
+
+def loopkv_paged_workspace(pool, desc):
+    nbytes = ctypes.c_size_t()
+    rc = _lib.loopkv_paged_workspace(_ref(pool), _ref(desc), ctypes.byref(nbytes))
+    return rc, nbytes.value
+
+
+def loopkv_paged_decode(pool, desc, h_cells, h_current, n_cells, d_table, d_len, q, cur_k, cur_v,
+                        d_out, d_lse, d_work, work_bytes, d_status, stream):
+    return _lib.loopkv_paged_decode(_ref(pool), _ref(desc), h_cells, h_current, n_cells, d_table,
+                                    d_len, _ref(q), _ref(cur_k), _ref(cur_v), d_out, d_lse, d_work,
+                                    work_bytes, d_status, stream)
 
 
 def loopkv_plan_optimize(desc, kinds_out):

@@ -1,0 +1,393 @@
+"""Paged cells: a key-value cache whose tokens live in pages.
+
+``page_map`` makes room for a step's new tokens (block tables and slot map from
+the request lengths), ``paged_append`` writes their keys and values,
+``paged_decode`` is the attention of each request's newest token over its
+pages, ``page_release`` gives pages back.  All state is in device tensors, so a
+step of these calls can be captured into a CUDA graph and replayed.
+``PagedCache`` keeps the tensors of one cache together.
+
+Argument marshalling only, as in ``loopkv``: the work runs in ``libloopkv.so``
+(``include/loopkv.h``, "Paged cells").  Checks here raise LoopKVError with
+LOOPKV_ERR_INVALID_ARG and launch nothing; what only the device data can show
+(no free page, a page id outside the pool) sets bits in ``status`` (int32 [1]).
+
+Shapes: pages [cells, pages, KV heads, page size, head dim] (bf16, fp16, or
+uint8 codes with ``meta`` fp32 [cells, pages, KV heads, page size, 4]); table
+int32 [batch, pages of the longest request]; slot = page * page size + offset.
+Vectors (q, k, v, cur_k, cur_v) are [listed cells, rows, heads, head dim] with
+contiguous channels; their other strides are free (multiples of 8 elements), so
+slices of a fused projection's output can be given as they are.
+"""
+
+import contextlib
+import ctypes
+
+import numpy as np
+
+from . import loopkv as _lk
+from .loopkv import _check, _invalid
+
+_FORMATS = None
+
+
+def _formats():
+    """Page dtype -> (format, dtype of the vectors)."""
+    global _FORMATS
+    if _FORMATS is None:
+        import torch
+        _FORMATS = {torch.bfloat16: (_lk.LOOPKV_PAGE_BF16, torch.bfloat16),
+                    torch.float16: (_lk.LOOPKV_PAGE_F16, torch.float16),
+                    torch.uint8: (_lk.LOOPKV_PAGE_Q8, torch.bfloat16)}
+    return _FORMATS
+
+
+_NOTHING = contextlib.nullcontext()
+
+
+def _place(where, device, stream):
+    """(context, stream handle) of a launch on ``device``: the stream given, or
+    the device's current one, with the device made current if it is not."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+        if stream.device_index == torch.cuda.current_device():
+            return _NOTHING, stream.cuda_stream
+        return torch.cuda.device(device), stream.cuda_stream
+    if stream.device != device:
+        raise _invalid(where, "the stream is on %s, the tensors on %s" % (stream.device, device))
+    return torch.cuda.stream(stream), stream.cuda_stream
+
+
+def _ints(t, where, name, device, shape):
+    """Pointer of a contiguous int32 tensor of a given shape."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise _invalid(where, "%s must be a torch tensor, not %s" % (name, type(t).__name__))
+    if t.device != device or not t.is_cuda:
+        raise _invalid(where, "%s must be on %s, not %s" % (
+            name, device if device.type == "cuda" else "a CUDA device", t.device))
+    if t.dtype != torch.int32:
+        raise _invalid(where, "%s must be torch.int32, not %s" % (name, t.dtype))
+    if tuple(t.shape) != shape:
+        raise _invalid(where, "%s must have shape %s, not %s" % (name, shape, tuple(t.shape)))
+    if not t.is_contiguous():
+        raise _invalid(where, "%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _status(status, where, device):
+    return None if status is None else _ints(status, where, "status", device, (1,))
+
+
+def _size(value, where, name):
+    if isinstance(value, bool) or int(value) != value or not 0 <= value < 1 << 31:
+        raise _invalid(where, "%s must be a count, not %r" % (name, value))
+    return int(value)
+
+
+def _shape(t, where, name, ndim):
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise _invalid(where, "%s must be a torch tensor, not %s" % (name, type(t).__name__))
+    if t.dim() != ndim:
+        raise _invalid(where, "%s must have %d dimensions, not %d" % (name, ndim, t.dim()))
+    return tuple(t.shape)
+
+
+def page_map(lengths, n_new, table, free, free_count, page_size, slots, starts, newest=None,
+             lengths_out=None, free_count_out=None, status=None, stream=None):
+    """Room for ``n_new`` [batch] new tokens of requests that hold ``lengths``
+    [batch]: pages from the end of ``free`` [pages of the pool] (the first
+    ``free_count`` [1] are free) are entered in ``table`` [batch, width];
+    ``slots`` [rows] gets the slot of every new token, request after request
+    (-1 behind the last and for refused requests), ``starts`` [batch + 1] the
+    first row of every request, ``newest`` [batch] (optional) the slot of its
+    last new token (-1: none).  New lengths and free count go to
+    ``lengths_out`` / ``free_count_out`` (None: in place).  A request that does
+    not fit (pages, table width, rows) is refused whole: its length stays and
+    ``status`` gets a bit.  Returns (slots, starts)."""
+    where = "page_map"
+    batch, width = _shape(table, where, "table", 2)
+    (n_pages,), (rows,) = _shape(free, where, "free", 1), _shape(slots, where, "slots", 1)
+    page_size = _size(page_size, where, "page_size")
+    dev = table.device
+    lengths_out = lengths if lengths_out is None else lengths_out
+    free_count_out = free_count if free_count_out is None else free_count_out
+    args = (_ints(lengths, where, "lengths", dev, (batch,)),
+            _ints(n_new, where, "n_new", dev, (batch,)),
+            _ints(table, where, "table", dev, (batch, width)),
+            _ints(free, where, "free", dev, (n_pages,)),
+            _ints(free_count, where, "free_count", dev, (1,)),
+            _ints(slots, where, "slots", dev, (rows,)),
+            _ints(starts, where, "starts", dev, (batch + 1,)),
+            None if newest is None else _ints(newest, where, "newest", dev, (batch,)),
+            _ints(lengths_out, where, "lengths_out", dev, (batch,)),
+            _ints(free_count_out, where, "free_count_out", dev, (1,)),
+            _status(status, where, dev))
+    context, handle = _place(where, dev, stream)
+    with context:
+        rc = _lk._lib.loopkv_page_map(batch, page_size, width, n_pages, rows, *args, handle)
+    _check(rc, "loopkv_page_map")
+    return slots, starts
+
+
+def page_release(lengths, new_lengths, table, free, free_count, page_size, lengths_out=None,
+                 free_count_out=None, status=None, stream=None):
+    """Cut requests from ``lengths`` [batch] to ``new_lengths`` [batch] tokens
+    (0: the request ended) and push the pages they no longer need to the end
+    of ``free``, request after request.  New lengths and free count go to
+    ``lengths_out`` / ``free_count_out`` (None: in place); the table stays as
+    it is.  A request whose new length is not in 0 .. its length keeps it."""
+    where = "page_release"
+    batch, width = _shape(table, where, "table", 2)
+    (n_pages,) = _shape(free, where, "free", 1)
+    page_size = _size(page_size, where, "page_size")
+    dev = table.device
+    lengths_out = lengths if lengths_out is None else lengths_out
+    free_count_out = free_count if free_count_out is None else free_count_out
+    args = (_ints(lengths, where, "lengths", dev, (batch,)),
+            _ints(new_lengths, where, "new_lengths", dev, (batch,)),
+            _ints(table, where, "table", dev, (batch, width)),
+            _ints(free, where, "free", dev, (n_pages,)),
+            _ints(free_count, where, "free_count", dev, (1,)),
+            _ints(lengths_out, where, "lengths_out", dev, (batch,)),
+            _ints(free_count_out, where, "free_count_out", dev, (1,)),
+            _status(status, where, dev))
+    context, handle = _place(where, dev, stream)
+    with context:
+        rc = _lk._lib.loopkv_page_release(batch, page_size, width, n_pages, *args, handle)
+    _check(rc, "loopkv_page_release")
+
+
+def _pool(k_pages, v_pages, meta, where):
+    """(loopkv_page_pool, dtype of the vectors) of the page tensors."""
+    import torch
+    shape = _shape(k_pages, where, "k_pages", 5)
+    if k_pages.dtype not in _formats():
+        raise _invalid(where, "k_pages must be torch.bfloat16, torch.float16 or torch.uint8, not %s"
+                       % k_pages.dtype)
+    fmt, dtype = _formats()[k_pages.dtype]
+    dev = k_pages.device
+    if not k_pages.is_cuda or not k_pages.is_contiguous():
+        raise _invalid(where, "k_pages must be contiguous and on a CUDA device, not on %s" % dev)
+    _lk._need(v_pages, where, "v_pages", (k_pages.dtype,), shape=shape, device=dev)
+    if (meta is None) != (fmt != _lk.LOOPKV_PAGE_Q8):
+        raise _invalid(where, "meta belongs to uint8 pages, and to no others")
+    if meta is not None:
+        _lk._need(meta, where, "meta", (torch.float32,), shape=shape[:4] + (4,), device=dev)
+    cells, pages, heads, page_size, dim = shape
+    return _lk.loopkv_page_pool(cells, pages, page_size, heads, dim, fmt, k_pages.data_ptr(),
+                                v_pages.data_ptr(), None if meta is None else meta.data_ptr()), dtype
+
+
+def _rows(t, where, name, dtype, device, shape):
+    """loopkv_rows of a [cells, rows, heads, head dim] tensor."""
+    got = _shape(t, where, name, 4)
+    if t.device != device:
+        raise _invalid(where, "%s must be on %s, not %s" % (name, device, t.device))
+    if t.dtype != dtype:
+        raise _invalid(where, "%s must be %s, not %s" % (name, dtype, t.dtype))
+    if any(w is not None and w != g for w, g in zip(shape, got)):
+        raise _invalid(where, "%s has shape %s; expected (%s)" % (
+            name, got, ", ".join("any" if w is None else str(w) for w in shape)))
+    strides = t.stride()
+    outer = [0 if n <= 1 else s for n, s in zip(got[:3], strides[:3])]
+    if strides[3] != 1 or any(s & 7 for s in outer) or t.data_ptr() & 15:
+        raise _invalid(where, "%s must have contiguous channels, strides that are multiples of 8 "
+                              "and start on a 16-byte boundary; its strides are %s" % (name, strides))
+    return _lk.loopkv_rows(t.data_ptr(), *outer)
+
+
+def _cells(cells, where):
+    """Host int32 array of a list of cells."""
+    a = np.ascontiguousarray(cells, dtype=np.int32).reshape(-1)
+    if not 1 <= a.size <= _lk.LOOPKV_MAX_CELLS_PER_CALL:
+        raise _invalid(where, "1 to %d cells in a call, not %d" % (
+            _lk.LOOPKV_MAX_CELLS_PER_CALL, a.size))
+    return a
+
+
+def paged_append(cells, k, v, slots, k_pages, v_pages, meta=None, status=None, stream=None):
+    """Write k, v [listed cells, rows, KV heads, head dim] of new tokens to
+    slots ``slots`` [rows] of pool cells ``cells`` (host; distinct; -1: nothing
+    is stored of that input).  Rows with slot -1 are skipped.  uint8 pages get
+    codes and ``meta`` their scales and zero points."""
+    where = "paged_append"
+    pool, dtype = _pool(k_pages, v_pages, meta, where)
+    dev = k_pages.device
+    cells = _cells(cells, where)
+    (rows,) = _shape(slots, where, "slots", 1)
+    shape = (cells.size, rows, pool.n_kv_heads, pool.head_dim)
+    kr = _rows(k, where, "k", dtype, dev, shape)
+    vr = _rows(v, where, "v", dtype, dev, shape)
+    d_slots = _ints(slots, where, "slots", dev, (rows,))
+    d_status = _status(status, where, dev)
+    context, handle = _place(where, dev, stream)
+    with context:
+        rc = _lk._lib.loopkv_paged_append(
+            ctypes.addressof(pool), cells.ctypes.data, cells.size, rows, d_slots,
+            ctypes.addressof(kr), ctypes.addressof(vr), d_status, handle)
+    _check(rc, "loopkv_paged_append")
+
+
+def paged_decode(cells, q, k_pages, v_pages, table, lengths, meta=None, cur_k=None, cur_v=None,
+                 current=None, out=None, lse=None, sm_scale=0.0, status=None, stream=None):
+    """Attention of one new token per request: q [listed cells, batch, query
+    heads, head dim] over the ``lengths`` [batch] tokens of each request's
+    pages in pool cells ``cells`` (host; a cell may be listed more than once).
+    Query head h * g + r reads KV head h (g = query heads / KV heads, 1 to 16).
+    With cur_k, cur_v [listed cells, batch, KV heads, head dim], the last token
+    of every request is read from them instead of its page, for all listed
+    cells or those where ``current`` (host, one truth value per listed cell) is
+    true.  Returns out in q's dtype and shape; ``lse`` (fp32 [listed cells,
+    batch, query heads]) receives the natural-log sum of exponentials.  A
+    request without tokens gives zeros and -infinity."""
+    import torch
+    where = "paged_decode"
+    pool, dtype = _pool(k_pages, v_pages, meta, where)
+    dev = k_pages.device
+    cells = _cells(cells, where)
+    batch, width = _shape(table, where, "table", 2)
+    heads, dim = pool.n_kv_heads, pool.head_dim
+    qr = _rows(q, where, "q", dtype, dev, (cells.size, batch, None, dim))
+    q_heads = q.shape[2]
+    if q_heads % heads or not 1 <= q_heads // heads <= _lk.LOOPKV_MAX_PAGED_GROUP:
+        raise _invalid(where, "%d query heads on %d KV heads: 1 to %d each" % (
+            q_heads, heads, _lk.LOOPKV_MAX_PAGED_GROUP))
+    d_table = _ints(table, where, "table", dev, (batch, width))
+    d_len = _ints(lengths, where, "lengths", dev, (batch,))
+    kr = vr = flags = None
+    if (cur_k is None) != (cur_v is None):
+        raise _invalid(where, "cur_k and cur_v come together")
+    if current is not None:
+        flags = np.ascontiguousarray(current, dtype=np.uint8).reshape(-1)
+        if flags.size != cells.size:
+            raise _invalid(where, "current must hold %d values, not %d" % (cells.size, flags.size))
+        if cur_k is None and flags.any():
+            raise _invalid(where, "cur_k and cur_v are required where current is true")
+    if cur_k is not None:
+        kr = _rows(cur_k, where, "cur_k", dtype, dev, (cells.size, batch, heads, dim))
+        vr = _rows(cur_v, where, "cur_v", dtype, dev, (cells.size, batch, heads, dim))
+        if flags is None:
+            flags = np.ones(cells.size, np.uint8)
+    desc = _lk.loopkv_paged_desc(batch, width, q_heads // heads, float(sm_scale))
+    d_status = _status(status, where, dev)
+    rc, nbytes = _lk.loopkv_paged_workspace(pool, desc)
+    _check(rc, "loopkv_paged_workspace")
+    context, handle = _place(where, dev, stream)
+    with context:  # memory made here belongs to the stream of the launch
+        if out is None:
+            out = torch.empty(tuple(q.shape), dtype=dtype, device=dev)
+        else:
+            _lk._need(out, where, "out", (dtype,), shape=q.shape, device=dev)
+        if lse is not None:
+            _lk._need(lse, where, "lse", (torch.float32,), shape=q.shape[:-1], device=dev)
+        work = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        rc = _lk._lib.loopkv_paged_decode(
+            ctypes.addressof(pool), ctypes.addressof(desc), cells.ctypes.data,
+            None if flags is None else flags.ctypes.data, cells.size, d_table, d_len,
+            ctypes.addressof(qr), None if kr is None else ctypes.addressof(kr),
+            None if vr is None else ctypes.addressof(vr), out.data_ptr(),
+            None if lse is None else lse.data_ptr(), work.data_ptr(), nbytes, d_status, handle)
+    _check(rc, "loopkv_paged_decode")
+    return out
+
+
+class PagedCache:
+    """The pages, block table, lengths and free list of one looped model's
+    cache.  Cells are loop-major (cell = loop * n_layers + layer); those in
+    ``shared`` (non-final loops only) store nothing and read the final loop's
+    pages of their layer with their own current token.  ``dtype``: torch
+    dtype of the pages (torch.uint8: 8-bit codes with scales)."""
+
+    def __init__(self, n_loops, n_layers, n_kv_heads, head_dim, n_pages, page_size, max_batch,
+                 max_pages, shared=(), dtype=None, sm_scale=0.0, device="cuda"):
+        import torch
+        where = "PagedCache"
+        dtype = torch.bfloat16 if dtype is None else dtype
+        if dtype not in _formats():
+            raise _invalid(where, "pages of %s" % dtype)
+        if n_loops < 1 or n_layers < 1:
+            raise _invalid(where, "%d loops of %d layers" % (n_loops, n_layers))
+        if not 1 <= max_batch <= _lk.LOOPKV_MAX_PAGED_BATCH or max_pages < 1 or \
+                max_pages * page_size > _lk.LOOPKV_MAX_PAGED_TOKENS:
+            raise _invalid(where, "%d requests of %d pages of %d tokens" % (
+                max_batch, max_pages, page_size))
+        self.n_loops, self.n_layers, self.n_cells = n_loops, n_layers, n_loops * n_layers
+        self.page_size, self.sm_scale = page_size, float(sm_scale)
+        self.shared = np.zeros(self.n_cells, bool)
+        for cell in shared:
+            if not 0 <= cell < self.n_cells - n_layers:
+                raise _invalid(where, "cell %d cannot share: only cells of non-final loops" % cell)
+            self.shared[cell] = True
+        # the pool cell of every cell: its own, or its layer's in the final loop
+        stored = np.cumsum(~self.shared, dtype=np.int32) - 1
+        final = np.tile(stored[self.n_cells - n_layers:], n_loops)
+        self.pool_cell = np.where(self.shared, final, stored).astype(np.int32)
+        self.store_cell = np.where(self.shared, -1, stored).astype(np.int32)
+        shape = (int(stored[-1]) + 1, n_pages, n_kv_heads, page_size, head_dim)
+        self.k_pages = torch.zeros(shape, dtype=dtype, device=device)
+        self.v_pages = torch.zeros(shape, dtype=dtype, device=device)
+        self.meta = None
+        if dtype == torch.uint8:
+            self.meta = torch.zeros(shape[:4] + (4,), dtype=torch.float32, device=device)
+        i32 = dict(dtype=torch.int32, device=device)
+        self.table = torch.full((max_batch, max_pages), -1, **i32)
+        self.lengths = torch.zeros(max_batch, **i32)
+        self.free = torch.arange(n_pages - 1, -1, -1, **i32)
+        self.free_count = torch.full((1,), n_pages, **i32)
+        self.starts = torch.zeros(max_batch + 1, **i32)
+        self.newest = torch.full((max_batch,), -1, **i32)
+        self.status = torch.zeros(1, **i32)
+
+    def _listed(self, cells, where):
+        cells = _cells(cells, where)
+        if cells.min() < 0 or cells.max() >= self.n_cells:
+            raise _invalid(where, "cells are 0 .. %d" % (self.n_cells - 1))
+        return cells
+
+    def grow(self, n_new, slots, stream=None):
+        """Room for n_new (int32 [max_batch] on the device) tokens per request;
+        fills slots (int32 [rows] on the device), ``starts`` and ``newest``;
+        returns slots."""
+        return page_map(self.lengths, n_new, self.table, self.free, self.free_count,
+                        self.page_size, slots, self.starts, newest=self.newest,
+                        status=self.status, stream=stream)[0]
+
+    def cut(self, new_lengths, stream=None):
+        """Cut every request to new_lengths (int32 [max_batch] on the device)."""
+        page_release(self.lengths, new_lengths, self.table, self.free, self.free_count,
+                     self.page_size, status=self.status, stream=stream)
+
+    def append(self, cells, k, v, slots, stream=None):
+        """k, v [cells, rows, KV heads, head dim] to ``slots``; shared cells keep nothing."""
+        cells = self._listed(cells, "PagedCache.append")
+        paged_append(self.store_cell[cells], k, v, slots, self.k_pages, self.v_pages, self.meta,
+                     status=self.status, stream=stream)
+
+    def decode(self, cells, q, cur_k=None, cur_v=None, out=None, lse=None, stream=None):
+        """q [cells, max_batch, query heads, head dim]; cur_k, cur_v [cells,
+        max_batch, KV heads, head dim] are needed if a listed cell is shared."""
+        where = "PagedCache.decode"
+        cells = self._listed(cells, where)
+        current = self.shared[cells]
+        if current.any() and (cur_k is None or cur_v is None):
+            raise _invalid(where, "shared cells read their current token: cur_k and cur_v")
+        return paged_decode(self.pool_cell[cells], q, self.k_pages, self.v_pages, self.table,
+                            self.lengths, meta=self.meta, cur_k=cur_k, cur_v=cur_v,
+                            current=current, out=out, lse=lse, sm_scale=self.sm_scale,
+                            status=self.status, stream=stream)
+
+    def check(self, stream=None):
+        """Wait for ``stream``, read and clear the status word; raises
+        LoopKVError (LOOPKV_ERR_CAPACITY if requests were refused for want of
+        room, else LOOPKV_ERR_DEVICE) when it is not 0."""
+        import torch
+        with torch.cuda.stream(stream):
+            bits = int(self.status.item())
+            if bits:
+                self.status.zero_()
+        if bits:
+            room = _lk.LOOPKV_PAGE_NO_TABLE | _lk.LOOPKV_PAGE_NO_ROWS | _lk.LOOPKV_PAGE_NO_PAGES
+            raise _lk.LoopKVError(6 if bits & ~room else 3, "PagedCache status 0x%x" % bits)

@@ -1,4 +1,5 @@
-"""One decode step of a looped model in serving order, on a loaded ``Plan``.
+"""One decode step of a looped model in serving order, on a loaded ``Plan`` or a
+``paged.PagedCache``.
 
 A looped transformer runs loop 0 over all layers, then loop 1, and so on; the
 final loop's KV is what SHARE cells reuse ("LoopKV: Loop-Aware KV Cache
@@ -8,7 +9,7 @@ token the cache sees: append + decode for the cells of the non-final loops
 previous step), then append + decode for the final loop.  Batching all cells
 of a phase into one launch is the throughput form of that order.
 
-Only library calls (``Plan.append``, ``Plan.decode``) are issued here.
+Only library calls are issued here.
 """
 
 import numpy as np
@@ -39,3 +40,22 @@ def decode_step(plan, phase_cells, q, k_new, v_new, out, lse=None, mask=None, ns
                     nsel=None if nsel is None else nsel[i], stream=stream)
         if events is not None:
             events[i][1].record(stream)
+
+
+def paged_decode_step(cache, phase_cells, ones, slots, q, k_new, v_new, out, lse=None, stream=None):
+    """The same step on a ``paged.PagedCache``: room for one token of every
+    request with ones[b] = 1 (int32 [batch] on the device; 0: the request
+    pauses, its outputs mean nothing), then append and decode, phase by phase.
+
+    For phase i: q[i] [cells, batch, query heads, D], k_new[i] / v_new[i]
+    [cells, batch, KV heads, D], out[i] like q[i]: row b is request b's.  slots:
+    int32 [batch] on the device, scratch.  Only library calls on device state:
+    a captured step can be replayed.
+    """
+    cache.grow(ones, slots, stream=stream)
+    for i, cells in enumerate(phase_cells):
+        cache.append(cells, k_new[i], v_new[i], cache.newest, stream=stream)
+        shares = cache.shared[cells].any()
+        cache.decode(cells, q[i], cur_k=k_new[i] if shares else None,
+                     cur_v=v_new[i] if shares else None, out=out[i],
+                     lse=None if lse is None else lse[i], stream=stream)
