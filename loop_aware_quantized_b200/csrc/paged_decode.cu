@@ -11,25 +11,28 @@
 //
 // What bounds it: the pages' bytes.  One new token does 4 g D flops on the
 // 4 D bytes (bf16) of a token, g flops a byte where the tensor pipe could
-// take 250, so the tokens are streamed from HBM straight into the registers
-// that mma.sync reads - no shared memory, no barrier in the loop, every warp
-// on its own - and the contraction costs a fraction of the issue slots.
+// take 250.  So every warp keeps its own ring of tiles in shared memory, filled
+// by cp.async two to four tiles ahead (an SM has 100 KB and more in flight, and
+// one latency of HBM at its share of the bandwidth is 50 KB), without a barrier
+// between warps; keys and values are separate groups, so a tile's keys are
+// replaced while its values are still used.  Rows behind a request's length
+// and rows of bad pages are filled with zeros and not read.
 //
 // Fragments (lane = 4 r + c).  Scores: m16n8k16 with the queries as A and 8
-// tokens as B; token r of an 8-token group is column r, and since the order of
-// the contraction is free, lane (r, c) reads 16 contiguous bytes of its
-// token, chunk c of 4, as the B operands of two steps.  The accumulator holds
-// queries r (and r + 8) x tokens 2c, 2c + 1, which is the layout of the B
-// operand of the second product out^T = V^T p^T: p needs no exchange.  Its A
-// operand pairs two tokens of one channel: lane (r, c) reads 16 bytes of
-// its tokens 2c, 2c + 1, 2c + 8, 2c + 9 (the row chunk r) and pairs
-// them with byte permutes.  Weights p are used as a sum of two 16-bit floats
+// tokens as B (ldmatrix).  The accumulator holds queries r (and r + 8) x
+// tokens 2c, 2c + 1, which is the layout of the B operand of the second
+// product out^T = V^T p^T: p needs no exchange.  Its A operand comes from
+// ldmatrix.trans.  Weights p are used as a sum of two 16-bit floats
 // (p = hi + lo up to 2^-16 p), so their rounding stays below that of a bf16
-// output: with g <= 4 the rows r + 4 of A repeat the queries and their lanes
-// take the lo part (no instruction more), otherwise a second product adds it.
+// output: with up to 4 query rows the rows r + 4 of A repeat the queries and
+// their lanes take the lo part (no instruction more), otherwise a second
+// product adds it.
 // hi is cut towards zero and lo kept above zero (kTiny, far below any weight's
 // rounding), so that an infinite value stays infinite and is no NaN.
 // fp16 weights are scaled by 2^14 so that small ones keep their bits.
+//
+// Cells that share.  Listed cells that read the same pool cell are one unit
+// with all their query rows (Sets), so their pages are read once.
 //
 // Q8 pages.  A byte code c moved into the low half of a bf16 pattern is the
 // (subnormal) bf16 c 2^-133, exactly; queries carry 2^64 and weights 2^64, so
@@ -49,6 +52,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <climits>
 #include <cmath>
 #include <cstdint>
 
@@ -59,14 +63,14 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kCtasPerSm = 3;
 constexpr int kSms = 148;
-constexpr int kWorkers = kSms * kCtasPerSm;
+constexpr int kMaxWorkers = kSms * 4;
 constexpr int kTile = 16;            // tokens of a warp's step
 constexpr int kMinTiles = 2 * kWarps;  // tiles a worker takes at least
-constexpr int kMaxGroup = LOOPKV_MAX_PAGED_GROUP;
+constexpr int kMaxRows = LOOPKV_MAX_PAGED_GROUP;  // query rows of a set
+constexpr int kJoinThreads = 512;
 constexpr uint32_t kNoRow = 0xffffffffu;
-constexpr int kCurrentBit = 1 << 30;  // in a cell list entry: the last token is in cur_k / cur_v
+constexpr int kCurrentBit = 1 << 30;  // in a set's cell: the last token is in cur_k / cur_v
 
 struct RowView {
   const uint16_t* data;
@@ -85,17 +89,23 @@ struct PagedDecodeParams {
   RowView q, cur_k, cur_v;
   uint16_t* out;
   float* lse;
-  float* part;        // [2 * workers][g][D + 2] partial results: out, m, l
+  float* part;        // [2 * workers][rows * (D + 2)] partial results: out, m, l
   int32_t* split;     // [workers][2]: a unit begun but not ended here, workers that continue it
   uint32_t* status;
-  int32_t n_cells, batch, heads, group, max_pages, n_pages, workers;
+  int32_t n_sets, batch, heads, group, max_pages, n_pages, workers;
+  int32_t rows;       // query rows of the largest set
   int64_t cell_rows;  // token rows of a pool cell
   float scale2;       // sm_scale * log2(e)
   PageDiv div;
 };
 
-struct Cells {
+// Listed cells that read the same pool cell in the same way, in sets of at
+// most kMaxRows query rows: members first[s] .. first[s + 1] - 1, row i of the
+// set being query row i % group of member i / group.
+struct Sets {
   int32_t cell[LOOPKV_MAX_CELLS_PER_CALL];
+  uint16_t first[LOOPKV_MAX_CELLS_PER_CALL + 1];
+  uint16_t member[LOOPKV_MAX_CELLS_PER_CALL];  // index in the caller's list
 };
 
 template <int FMT>
@@ -160,51 +170,77 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) {
   return __byte_perm(a, b, s);
 }
 
-__device__ __forceinline__ uint4 load16(const uint8_t* p, bool on) {
-  uint4 x = make_uint4(0, 0, 0, 0);
-  if (on)
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-        : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "l"(p));
-  return x;
+__device__ __forceinline__ uint32_t shared_at(const void* p) {
+  return (uint32_t)__cvta_generic_to_shared(p);
 }
-__device__ __forceinline__ uint2 load8(const uint8_t* p, bool on) {
-  uint2 x = make_uint2(0, 0);
-  if (on)
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(x.x), "=r"(x.y) : "l"(p));
-  return x;
+// 16 bytes to shared memory; `on` false: zeros, and nothing is read
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+  __syncwarp();
+}
+__device__ __forceinline__ void ldsm(uint32_t (&w)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void ldsm_trans(uint32_t (&w)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
 }
 
-// The words a lane holds of one token row (16 bytes of every 64, Q8: the
-// same channels as bytes) and of one value row (its 16-byte pieces).
-template <int D, int FMT>
+// A warp's tile in shared memory: key rows, value rows, Q8: meta.  16-byte
+// piece x of row t lies at piece x ^ swizzle(t), so that the 8 rows of an
+// ldmatrix read 8 different banks' worth.
+template <int D, int FMT, int MODE>
 struct Shape {
   static constexpr bool kQ8 = FMT == LOOPKV_PAGE_Q8;
   static constexpr int kRowBytes = kQ8 ? D : 2 * D;
+  static constexpr int kPieces = kRowBytes / 16;
+  static constexpr int kRowsPerCopy = 32 / kPieces;    // rows one instruction of a warp copies
+  static constexpr int kCopies = kTile / kRowsPerCopy;
   static constexpr int kSteps = D / 16;        // contraction steps of the scores
   static constexpr int kMTiles = D / 16;       // 16-channel tiles of the output
-  static constexpr int kKeyWords = kRowBytes / 16;    // 32-bit words a lane holds of a key token
-  static constexpr int kValueWords = kRowBytes / 32;  // and of a value token
+  static constexpr int kRowsBytes = kTile * kRowBytes;
+  static constexpr int kTileBytes = 2 * kRowsBytes + (kQ8 ? 16 * kTile : 0);
+  static constexpr int kStages = kTileBytes > 8000 ? 2 : (kTileBytes > 4000 ? 3 : 4);
+  static constexpr int kWarpBytes = kStages * kTileBytes;
+  static constexpr int kCtasPerSm = (kTileBytes > 8000 || (MODE == 2 && D == 128)) ? 3 : 4;
+  static constexpr int kWorkers = kSms * kCtasPerSm;
+  static __device__ __forceinline__ int swizzle(int t) { return kPieces == 4 ? (t >> 1) & 3 : t & 7; }
 };
 
-template <int D, int FMT, int MODE>  // MODE 0: g <= 4, 1: g <= 8, 2: g <= 16
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
-paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_constant__ Cells cells) {
+template <int D, int FMT, int MODE>  // MODE 0: up to 4 query rows, 1: 8, 2: 16
+__global__ void __launch_bounds__(kThreads, Shape<D, FMT, MODE>::kCtasPerSm)
+paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_constant__ Sets sets) {
   require_ieee_subnormals();
-  using S = Shape<D, FMT>;
+  using S = Shape<D, FMT, MODE>;
   using M = Mma<FMT>;
   constexpr bool Q8 = S::kQ8;
   constexpr int NT = MODE == 2 ? 2 : 1;      // query halves (8 columns of out^T each)
   constexpr int ROWS = 8 * NT;               // query rows a warp keeps
   constexpr int OS = D + 4;                  // floats of a row in shared memory (banks)
-  extern __shared__ __align__(16) uint8_t smem[];
-  float* const so = reinterpret_cast<float*>(smem);               // [kWarps][ROWS][OS]
-  float* const sm = so + kWarps * ROWS * OS;                      // [kWarps + 1][ROWS] maxima
-  float* const sl = sm + (kWarps + 1) * kMaxGroup;                // [kWarps + 1][ROWS] sums
-  float* const sz = sl + (kWarps + 1) * kMaxGroup;                // [kWarps][ROWS] zero-point sums (Q8)
-  int* const prefix = reinterpret_cast<int*>(sz + kWarps * kMaxGroup);  // [batch + 1] tiles before a request
+  static_assert(ROWS * OS * 4 <= S::kWarpBytes, "a warp's results take the place of its tiles");
+  extern __shared__ __align__(128) uint8_t smem[];
+  float* const sm = reinterpret_cast<float*>(smem + kWarps * S::kWarpBytes);  // [kWarps + 1][kMaxRows] maxima
+  float* const sl = sm + (kWarps + 1) * kMaxRows;                // sums
+  float* const sz = sl + (kWarps + 1) * kMaxRows;                // [kWarps][kMaxRows] zero-point sums (Q8)
+  int* const prefix = reinterpret_cast<int*>(sz + kWarps * kMaxRows);  // [batch + 1] tiles before a request
   __shared__ int warp_sums[kWarps];
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
+  uint8_t* const ring = smem + warp * S::kWarpBytes;
+  const uint32_t ring_at = shared_at(ring);
+  // where this lane copies to and reads from, within a row and a tile
+  const int piece = lane % S::kPieces, copy_row = lane / S::kPieces;
+  const int k_row = (lane & 7) + ((lane >> 4) << 3), k_piece = (lane >> 3) & 1;  // tokens 0-7 | 8-15 x 2 pieces
+  const int v_row = (lane & 7) + (Q8 ? ((lane >> 3) & 1) << 3 : (lane >> 4) << 3);
+  const int v_piece = Q8 ? lane >> 4 : (lane >> 3) & 1;
   uint32_t status = 0;
 
   // Tiles of every request (at least one: a unit without tokens is written too).
@@ -242,7 +278,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
     }
     __syncthreads();
   }
-  const int per_request = p.n_cells * p.heads;
+  const int per_request = p.n_sets * p.heads;
   const int64_t all = (int64_t)prefix[p.batch] * per_request;
   const int64_t want = (all + kMinTiles - 1) / kMinTiles;
   const int workers = (int)(want < p.workers ? want : p.workers);
@@ -265,13 +301,71 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
     const int tiles = prefix[b + 1] - prefix[b];
     const int64_t rem = x - (int64_t)prefix[b] * per_request;
     const int u = (int)(rem / tiles), t0 = (int)(rem - (int64_t)u * tiles);
-    const int ci = u / p.heads, h = u - ci * p.heads;
+    const int set = u / p.heads, h = u - set * p.heads;
     const int t1 = (int)min((int64_t)tiles, t0 + (x1 - x));
+    const int first = sets.first[set], rows = (sets.first[set + 1] - first) * p.group;
     int n = p.len[b];
     if (n < 0 || n > p.max_pages * p.div.size) n = 0;
-    const bool current = (cells.cell[ci] & kCurrentBit) != 0 && n > 0;
-    const int cell = cells.cell[ci] & ~kCurrentBit;
+    const bool current = (sets.cell[set] & kCurrentBit) != 0 && n > 0;
+    const int64_t cell_row = (int64_t)(sets.cell[set] & ~kCurrentBit) * p.cell_rows + (int64_t)h * p.div.size;
     const int np = current ? n - 1 : n;  // tokens read from pages
+
+    // The page of token (lane & 15) of a tile (-1: no such token), loaded a
+    // step before its row is needed.
+    const int32_t* const entry = p.table + (int64_t)b * p.max_pages;
+    auto page_of = [&](int tile) -> int {
+      const int pos = tile * kTile + (lane & 15);
+      return tile < t1 && pos < np ? __ldg(entry + p.div.page(pos)) : INT_MIN;
+    };
+    auto row_of = [&](int tile, int page) -> uint32_t {
+      if (page == INT_MIN) return kNoRow;
+      if (page < 0 || page >= p.n_pages) {
+        status |= LOOPKV_PAGE_BAD_PAGE;
+        return kNoRow;
+      }
+      const int pos = tile * kTile + (lane & 15), off = pos - p.div.page(pos) * p.div.size;
+      return (uint32_t)(cell_row + (int64_t)page * p.heads * p.div.size + off);
+    };
+    auto copy_rows = [&](uint32_t at, const uint8_t* src, uint32_t row) {
+#pragma unroll
+      for (int i = 0; i < S::kCopies; ++i) {
+        const int t = i * S::kRowsPerCopy + copy_row;
+        const uint32_t from = __shfl_sync(0xffffffffu, row, t);
+        const bool on = from != kNoRow;
+        copy16(at + t * S::kRowBytes + ((piece ^ S::swizzle(t)) << 4),
+               src + (on ? (uint64_t)from * S::kRowBytes + 16 * piece : 0), on);
+      }
+    };
+    auto copy_keys = [&](int stage, uint32_t row) {
+      const uint32_t at = ring_at + stage * S::kTileBytes;
+      copy_rows(at, p.k, row);
+      if (Q8 && lane < kTile) {
+        const bool on = row != kNoRow;
+        copy16(at + 2 * S::kRowsBytes + 16 * lane, reinterpret_cast<const uint8_t*>(p.meta) + (on ? (uint64_t)row * 16 : 0), on);
+      }
+      copy_commit();
+    };
+    auto copy_values = [&](int stage, uint32_t row) {
+      copy_rows(ring_at + stage * S::kTileBytes + S::kRowsBytes, p.v, row);
+      copy_commit();
+    };
+
+    // The first tiles' copies; valid holds 16 bits a stage, this step's lowest.
+    uint64_t valid = 0;
+    int next_page;
+    {
+      int pages[S::kStages];
+#pragma unroll
+      for (int s = 0; s < S::kStages; ++s) pages[s] = page_of(t0 + warp + s * kWarps);
+      next_page = page_of(t0 + warp + S::kStages * kWarps);
+#pragma unroll
+      for (int s = 0; s < S::kStages; ++s) {
+        const uint32_t row = row_of(t0 + warp + s * kWarps, pages[s]);
+        copy_keys(s, row);
+        copy_values(s, row);
+        valid |= (uint64_t)(__ballot_sync(0xffffffffu, row != kNoRow) & 0xffffu) << (16 * s);
+      }
+    }
 
     // Query fragments.
     uint32_t qa[S::kSteps][MODE == 2 ? 4 : 2];
@@ -279,41 +373,38 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
 #pragma unroll
     for (int half = 0; half < NT; ++half) {
       const int row = MODE == 0 ? (r & 3) : r + 8 * half;
-      const bool on = row < p.group;
-      const uint16_t* src = p.q.at(ci, b, h * p.group + (on ? row : 0));
+      const bool on = row < rows;
+      const int mem = on ? row / p.group : 0;
+      const uint16_t* src = p.q.at(sets.member[first + mem], b, h * p.group + (on ? row - mem * p.group : 0));
       float sum = 0.f;
-      if constexpr (!Q8) {
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          const uint4 w = load16(reinterpret_cast<const uint8_t*>(src + 32 * i + 8 * c), on);
-          if constexpr (MODE == 2) {
-            qa[2 * i][half] = w.x;
-            qa[2 * i][2 + half] = w.y;
-            qa[2 * i + 1][half] = w.z;
-            qa[2 * i + 1][2 + half] = w.w;
-          } else {
-            qa[2 * i][0] = w.x;
-            qa[2 * i][1] = w.y;
-            qa[2 * i + 1][0] = w.z;
-            qa[2 * i + 1][1] = w.w;
+      for (int i = 0; i < S::kSteps; ++i) {
+        uint32_t w0 = 0, w1 = 0;
+        if constexpr (!Q8) {
+          if (on) {
+            w0 = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * i + 2 * c));
+            w1 = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * i + 8 + 2 * c));
           }
-        }
-      } else {
-        // a 16-byte piece of codes holds 16 channels: 16 c + 64 i ..
-#pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
-          const uint4 w0 = load16(reinterpret_cast<const uint8_t*>(src + 64 * i + 16 * c), on);
-          const uint4 w1 = load16(reinterpret_cast<const uint8_t*>(src + 64 * i + 16 * c + 8), on);
-          const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float a = M::lo(w[k]), z = M::hi(w[k]);
-            sum += a + z;
-            const uint32_t scaled = M::pack(a * 0x1p64f, z * 0x1p64f);
-            if constexpr (MODE == 2) qa[4 * i + k / 2][2 * (k & 1) + half] = scaled;
-            else qa[4 * i + k / 2][k & 1] = scaled;
+        } else {
+          // a lane's 4 codes of a 16-byte piece are channels 4 c ..
+          if (on) {
+            const uint2 w = __ldg(reinterpret_cast<const uint2*>(src + 16 * i + 4 * c));
+            w0 = w.x;
+            w1 = w.y;
           }
+          sum += (M::lo(w0) + M::hi(w0)) + (M::lo(w1) + M::hi(w1));
+          w0 = M::pack(M::lo(w0) * 0x1p64f, M::hi(w0) * 0x1p64f);
+          w1 = M::pack(M::lo(w1) * 0x1p64f, M::hi(w1) * 0x1p64f);
         }
+        if constexpr (MODE == 2) {
+          qa[i][half] = w0;
+          qa[i][2 + half] = w1;
+        } else {
+          qa[i][0] = w0;
+          qa[i][1] = w1;
+        }
+      }
+      if constexpr (Q8) {
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
       }
@@ -332,86 +423,51 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
         for (int k = 0; k < 4; ++k) o[half][j][k] = 0.f;
     }
 
-    // Token row of the tile's token (lane & 15), or kNoRow.
-    auto row_of = [&](int tile) -> uint32_t {
-      const int pos = tile * kTile + (lane & 15);
-      if (tile >= t1 || pos >= np) return kNoRow;
-      const int j = p.div.page(pos);
-      const int page = p.table[(int64_t)b * p.max_pages + j];
-      if (page < 0 || page >= p.n_pages) {
-        status |= LOOPKV_PAGE_BAD_PAGE;
-        return kNoRow;
-      }
-      return (uint32_t)((int64_t)cell * p.cell_rows + ((int64_t)page * p.heads + h) * p.div.size +
-                        (pos - j * p.div.size));
-    };
-
-    uint32_t row = row_of(t0 + warp);
+    int stage = 0;
     for (int tile = t0 + warp; tile < t1; tile += kWarps) {
-      // Loads: keys of tokens r and r + 8, values of tokens 2c, 2c + 1, 2c + 8, 2c + 9.
-      uint32_t kw[2][S::kKeyWords], vw[4][S::kValueWords];
-      bool on[2][2];
-      float4 meta[2][2];
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const uint32_t kr = __shfl_sync(0xffffffffu, row, r + 8 * g);
-        const uint8_t* src = p.k + (uint64_t)kr * S::kRowBytes + 16 * c;
-#pragma unroll
-        for (int i = 0; i < S::kKeyWords / 4; ++i) {
-          const uint4 w = load16(src + 64 * i, kr != kNoRow);
-          kw[g][4 * i] = w.x;
-          kw[g][4 * i + 1] = w.y;
-          kw[g][4 * i + 2] = w.z;
-          kw[g][4 * i + 3] = w.w;
-        }
-      }
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const uint32_t vr = __shfl_sync(0xffffffffu, row, 2 * c + (g & 1) + 8 * (g >> 1));
-        on[g >> 1][g & 1] = vr != kNoRow;
-        if constexpr (Q8) {
-          meta[g >> 1][g & 1] = vr != kNoRow ? __ldg(p.meta + vr) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        if constexpr (S::kValueWords == 2) {
-          const uint2 w = load8(p.v + (uint64_t)vr * S::kRowBytes + 8 * r, vr != kNoRow);
-          vw[g][0] = w.x;
-          vw[g][1] = w.y;
-        } else {
-          const uint8_t* src = p.v + (uint64_t)vr * S::kRowBytes + 16 * r;
-#pragma unroll
-          for (int i = 0; i < S::kValueWords / 4; ++i) {
-            const uint4 w = load16(src + 128 * i, vr != kNoRow);
-            vw[g][4 * i] = w.x;
-            vw[g][4 * i + 1] = w.y;
-            vw[g][4 * i + 2] = w.z;
-            vw[g][4 * i + 3] = w.w;
-          }
-        }
-      }
-      row = row_of(tile + kWarps);
+      const uint32_t keys = ring_at + stage * S::kTileBytes, values = keys + S::kRowsBytes;
+      copy_wait<2 * S::kStages - 1>();
 
       // Scores.
       float s[2][4];
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        s[g][0] = s[g][1] = s[g][2] = s[g][3] = 0.f;
+      for (int g = 0; g < 2; ++g) s[g][0] = s[g][1] = s[g][2] = s[g][3] = 0.f;
+      auto score = [&](int g, int ks, uint32_t b0, uint32_t b1) {
+        if constexpr (MODE == 2) M::run(s[g], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], b0, b1);
+        else M::run(s[g], qa[ks][0], 0u, qa[ks][1], 0u, b0, b1);
+      };
 #pragma unroll
-        for (int ks = 0; ks < S::kSteps; ++ks) {
-          uint32_t b0, b1;
-          if constexpr (Q8) {
-            const uint32_t w = kw[g][ks];
-            b0 = prmt(w, 0, 0x4140);
-            b1 = prmt(w, 0, 0x4342);
-          } else {
-            b0 = kw[g][2 * ks];
-            b1 = kw[g][2 * ks + 1];
-          }
-          if constexpr (MODE == 2) M::run(s[g], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], b0, b1);
-          else M::run(s[g], qa[ks][0], 0u, qa[ks][1], 0u, b0, b1);
+      for (int i = 0; i < S::kPieces / 2; ++i) {
+        uint32_t w[4];  // tokens 0-7: pieces 2 i, 2 i + 1; tokens 8-15: the same
+        ldsm(w, keys + k_row * S::kRowBytes + (((2 * i + k_piece) ^ S::swizzle(k_row)) << 4));
+        if constexpr (Q8) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            score(k >> 1, 2 * i + (k & 1), prmt(w[k], 0, 0x4140), prmt(w[k], 0, 0x4342));
+        } else {
+          score(0, i, w[0], w[1]);
+          score(1, i, w[2], w[3]);
         }
       }
+      float4 meta[2][2];
+      if constexpr (Q8) {
+        const float4* src = reinterpret_cast<const float4*>(ring + stage * S::kTileBytes + 2 * S::kRowsBytes);
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) meta[g][k] = src[2 * c + k + 8 * g];
+      }
+      const uint32_t bits = (uint32_t)valid >> (2 * c);
+      const bool on[2][2] = {{(bits & 1) != 0, (bits & 2) != 0}, {(bits & 0x100) != 0, (bits & 0x200) != 0}};
+      __syncwarp();
+      const int ahead = tile + S::kStages * kWarps;
+      const uint32_t row = row_of(ahead, next_page);
+      next_page = page_of(ahead + kWarps);
+      copy_keys(stage, row);
+      valid = valid >> 16 | (uint64_t)(__ballot_sync(0xffffffffu, row != kNoRow) & 0xffffu) << (16 * (S::kStages - 1));
 
       // Weights, 4 tokens of a query row per lane.
+      uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
       for (int half = 0; half < NT; ++half) {
         float e[2][2];
@@ -458,46 +514,52 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
               e[g][k] *= meta[g][k].z * 0x1p64f;
             }
           }
-        uint32_t ph[2], pl[2];
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          ph[g] = M::pack_down(e[g][0], e[g][1]);
-          pl[g] = M::pack(fmaxf(e[g][0] - M::lo(ph[g]), M::kTiny), fmaxf(e[g][1] - M::hi(ph[g]), M::kTiny));
-          if (MODE == 0 && r >= 4) ph[g] = pl[g];
+          ph[half][g] = M::pack_down(e[g][0], e[g][1]);
+          pl[half][g] = M::pack(fmaxf(e[g][0] - M::lo(ph[half][g]), M::kTiny), fmaxf(e[g][1] - M::hi(ph[half][g]), M::kTiny));
+          if (MODE == 0 && r >= 4) ph[half][g] = pl[half][g];
         }
+      }
 
-        // out^T += V^T p^T
-        if constexpr (!Q8) {
-          // tile j: rows r <-> channel 8 r + j of the first piece, rows r + 8
-          // <-> of the second (D = 64: channels 4 higher of the only one)
+      // out^T += V^T p^T
+      copy_wait<2 * S::kStages - 1>();
 #pragma unroll
-          for (int j = 0; j < S::kMTiles; ++j) {
-            const uint32_t sel = (j & 1) ? 0x7632 : 0x5410;
-            const int w0 = j / 2, w1 = D == 128 ? 4 + j / 2 : 2 + j / 2;
-            const uint32_t a0 = prmt(vw[0][w0], vw[1][w0], sel), a1 = prmt(vw[0][w1], vw[1][w1], sel);
-            const uint32_t a2 = prmt(vw[2][w0], vw[3][w0], sel), a3 = prmt(vw[2][w1], vw[3][w1], sel);
-            M::run(o[half][j], a0, a1, a2, a3, ph[0], ph[1]);
-            if constexpr (MODE != 0) M::run(o[half][j], a0, a1, a2, a3, pl[0], pl[1]);
+      for (int i = 0; i < S::kPieces / 2; ++i) {
+        uint32_t w[4];
+        ldsm_trans(w, values + v_row * S::kRowBytes + (((2 * i + v_piece) ^ S::swizzle(v_row)) << 4));
+        if constexpr (!Q8) {
+          // tile i: rows r, r + 8 are channels 16 i + r, 16 i + 8 + r
+#pragma unroll
+          for (int half = 0; half < NT; ++half) {
+            M::run(o[half][i], w[0], w[1], w[2], w[3], ph[half][0], ph[half][1]);
+            if constexpr (MODE != 0) M::run(o[half][i], w[0], w[1], w[2], w[3], pl[half][0], pl[half][1]);
           }
         } else {
-          // D = 128: 16 codes of the row, channels 16 r + j and 16 r + 8 + j;
-          // D = 64: 8 codes, channels 8 r + j and 8 r + 4 + j
+          // tile j: rows r, r + 8 are channels 16 j + 2 r, 16 j + 2 r + 1, the
+          // low and the high bytes of a pair
 #pragma unroll
-          for (int j = 0; j < S::kMTiles; ++j) {
-            const int w0 = j / 4, w1 = S::kMTiles / 4 + j / 4;
-            const uint32_t k = j & 3, sel = k | (4 + k) << 4;  // byte k of each token's word
-            const uint32_t x0 = prmt(vw[0][w0], vw[1][w0], sel), x1 = prmt(vw[0][w1], vw[1][w1], sel);
-            const uint32_t x2 = prmt(vw[2][w0], vw[3][w0], sel), x3 = prmt(vw[2][w1], vw[3][w1], sel);
-            const uint32_t a0 = prmt(x0, 0, 0x4140), a1 = prmt(x1, 0, 0x4140);
-            const uint32_t a2 = prmt(x2, 0, 0x4140), a3 = prmt(x3, 0, 0x4140);
-            M::run(o[half][j], a0, a1, a2, a3, ph[0], ph[1]);
-            if constexpr (MODE != 0) M::run(o[half][j], a0, a1, a2, a3, pl[0], pl[1]);
+          for (int k = 0; k < 2; ++k) {
+            const int j = 2 * i + k;
+            const uint32_t a0 = prmt(w[2 * k], 0, 0x4240), a1 = prmt(w[2 * k], 0, 0x4341);
+            const uint32_t a2 = prmt(w[2 * k + 1], 0, 0x4240), a3 = prmt(w[2 * k + 1], 0, 0x4341);
+#pragma unroll
+            for (int half = 0; half < NT; ++half) {
+              M::run(o[half][j], a0, a1, a2, a3, ph[half][0], ph[half][1]);
+              if constexpr (MODE != 0) M::run(o[half][j], a0, a1, a2, a3, pl[half][0], pl[half][1]);
+            }
           }
         }
       }
+      __syncwarp();
+      copy_values(stage, row);
+      stage = stage + 1 == S::kStages ? 0 : stage + 1;
     }
+    copy_wait<0>();  // empty groups only
 
     // Join the warps.
+    float* const so = reinterpret_cast<float*>(ring);
+    auto so_of = [&](int w) { return reinterpret_cast<const float*>(smem + w * S::kWarpBytes); };
 #pragma unroll
     for (int half = 0; half < NT; ++half) {
       l[half] += __shfl_xor_sync(0xffffffffu, l[half], 1);
@@ -507,31 +569,30 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
         z[half] += __shfl_xor_sync(0xffffffffu, z[half], 2);
       }
       if (c == 0) {
-        sm[warp * kMaxGroup + r + 8 * half] = m[half];
-        sl[warp * kMaxGroup + r + 8 * half] = l[half];
-        if constexpr (Q8) sz[warp * kMaxGroup + r + 8 * half] = z[half];
+        sm[warp * kMaxRows + r + 8 * half] = m[half];
+        sl[warp * kMaxRows + r + 8 * half] = l[half];
+        if constexpr (Q8) sz[warp * kMaxRows + r + 8 * half] = z[half];
       }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        float* dst = so + (warp * ROWS + 2 * c + k + 8 * half) * OS;
+        float* dst = so + (2 * c + k + 8 * half) * OS;
 #pragma unroll
         for (int j = 0; j < S::kMTiles; ++j) {
-          const float f = Q8 ? 0x1p69f : 1.f;
           if constexpr (!Q8) {
-            dst[8 * r + j] = o[half][j][k] * f;
-            dst[D == 128 ? 64 + 8 * r + j : 8 * r + 4 + j] = o[half][j][2 + k] * f;
+            dst[16 * j + r] = o[half][j][k];
+            dst[16 * j + 8 + r] = o[half][j][2 + k];
           } else {
-            dst[(D / 8) * r + j] = o[half][j][k] * f;
-            dst[(D / 8) * r + D / 16 + j] = o[half][j][2 + k] * f;
+            *reinterpret_cast<float2*>(dst + 16 * j + 2 * r) = make_float2(o[half][j][k] * 0x1p69f, o[half][j][2 + k] * 0x1p69f);
           }
         }
       }
     }
     const bool with_current = current && t1 == tiles;
     if (with_current) {
-      for (int g = warp; g < p.group; g += kWarps) {
-        const uint16_t* q = p.q.at(ci, b, h * p.group + g);
-        const uint16_t* k = p.cur_k.at(ci, b, h);
+      for (int i = warp; i < rows; i += kWarps) {
+        const int mem = i / p.group, li = sets.member[first + mem];
+        const uint16_t* q = p.q.at(li, b, h * p.group + i - mem * p.group);
+        const uint16_t* k = p.cur_k.at(li, b, h);
         float dot = 0.f;
         for (int d = 2 * lane; d < D; d += 64) {
           const uint32_t a = *reinterpret_cast<const uint32_t*>(q + d);
@@ -541,54 +602,51 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
         }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
-        if (lane == 0) {
-          sm[kWarps * kMaxGroup + g] = dot * p.scale2;
-          sl[kWarps * kMaxGroup + g] = 1.f;
-        }
+        if (lane == 0) sm[kWarps * kMaxRows + i] = dot * p.scale2;
       }
     }
     __syncthreads();
     const bool whole = t0 == 0 && t1 == tiles;
-    const int64_t unit = ((int64_t)ci * p.batch + b) * p.heads + h;
-    float* const part = p.part + (int64_t)(2 * me + (t0 == 0 ? 1 : 0)) * p.group * (D + 2);
-    for (int idx = tid; idx < p.group * D; idx += kThreads) {
-      const int g = idx / D, d = idx - g * D;
-      float top = with_current ? sm[kWarps * kMaxGroup + g] : -INFINITY;
+    float* const part = p.part + (int64_t)(2 * me + (t0 == 0 ? 1 : 0)) * p.rows * (D + 2);
+    for (int idx = tid; idx < rows * D; idx += kThreads) {
+      const int i = idx / D, d = idx - i * D;
+      const int mem = i / p.group, li = sets.member[first + mem];
+      float top = with_current ? sm[kWarps * kMaxRows + i] : -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[w * kMaxGroup + g]);
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[w * kMaxRows + i]);
       const float base = top == -INFINITY ? 0.f : top;
       float sum = 0.f, acc = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float f = exp2_fast(sm[w * kMaxGroup + g] - base);
-        sum = fmaf(f, sl[w * kMaxGroup + g], sum);
-        float y = so[(w * ROWS + g) * OS + d];
-        if constexpr (MODE == 0) y += so[(w * ROWS + g + 4) * OS + d];
-        if constexpr (Q8) y += sz[w * kMaxGroup + g];
+        const float f = exp2_fast(sm[w * kMaxRows + i] - base);
+        sum = fmaf(f, sl[w * kMaxRows + i], sum);
+        float y = so_of(w)[i * OS + d];
+        if constexpr (MODE == 0) y += so_of(w)[(i + 4) * OS + d];
+        if constexpr (Q8) y += sz[w * kMaxRows + i];
         acc = fmaf(f, y, acc);
       }
       if (with_current) {
-        const float f = exp2_fast(sm[kWarps * kMaxGroup + g] - base);
+        const float f = exp2_fast(sm[kWarps * kMaxRows + i] - base);
         sum += f;
-        acc = fmaf(f, M::lo(p.cur_v.at(ci, b, h)[d]), acc);
+        acc = fmaf(f, M::lo(p.cur_v.at(li, b, h)[d]), acc);
       }
       if (whole) {
+        const int64_t to = (((int64_t)li * p.batch + b) * p.heads + h) * p.group + i - mem * p.group;
         const float y = sum == 0.f ? 0.f : acc / sum;
-        p.out[(unit * p.group + g) * D + d] = (uint16_t)(M::pack(y, y) & 0xffffu);
-        if (d == 0 && p.lse)
-          p.lse[unit * p.group + g] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+        p.out[to * D + d] = (uint16_t)(M::pack(y, y) & 0xffffu);
+        if (d == 0 && p.lse) p.lse[to] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
       } else {
-        part[g * D + d] = acc;
+        part[idx] = acc;
         if (d == 0) {
-          part[p.group * D + g] = top;
-          part[p.group * (D + 1) + g] = sum;
+          part[p.rows * D + i] = top;
+          part[p.rows * (D + 1) + i] = sum;
         }
       }
     }
     if (!whole && t0 == 0 && tid == 0) {
       // the workers behind this one that hold the rest of the unit
       const int64_t last = x + tiles - 1;
-      p.split[2 * me] = (int)(unit);
+      p.split[2 * me] = (set * p.batch + b) * p.heads + h;
       p.split[2 * me + 1] = (int)(((last + 1) * workers - 1) / all) - me;
     }
     __syncthreads();  // shared memory is free for the next unit
@@ -600,64 +658,100 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
 
 // Join the parts of a unit that worker blockIdx.x began and did not end:
 // its own (slot 2 i + 1) and those of the workers behind it (slots 2 (i + k)).
+// A block does one query row, its threads the channels and kJoinThreads / D
+// interleaved shares of the parts.  Launched while the decode still runs
+// (every block waits for its end before it reads).
 template <int D, int FMT>
-__global__ void __launch_bounds__(D)
-paged_join_kernel(const __grid_constant__ PagedDecodeParams p) {
+__global__ void __launch_bounds__(kJoinThreads)
+paged_join_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_constant__ Sets sets) {
   using M = Mma<FMT>;
-  const int i = blockIdx.x, g = blockIdx.y, d = threadIdx.x;
+  constexpr int SLICES = kJoinThreads / D;
+  __shared__ float st[SLICES], sl[SLICES], sa[SLICES][D];
+  const int i = blockIdx.x, row = blockIdx.y, d = threadIdx.x % D, slice = threadIdx.x / D;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int more = p.split[2 * i + 1];
   if (more == 0) return;
-  const int64_t unit = (uint32_t)p.split[2 * i];
-  const int64_t stride = (int64_t)p.group * (D + 2);
-  auto slot = [&](int k) { return p.part + (k == 0 ? 2 * i + 1 : 2 * (i + k)) * stride; };
-  float top = -INFINITY;
-  for (int k = 0; k <= more; ++k) top = fmaxf(top, slot(k)[p.group * D + g]);
-  const float base = top == -INFINITY ? 0.f : top;
-  float sum = 0.f, acc = 0.f;
-  for (int k = 0; k <= more; ++k) {
-    const float* s = slot(k);
-    const float f = exp2_fast(s[p.group * D + g] - base);
-    sum = fmaf(f, s[p.group * (D + 1) + g], sum);
-    acc = fmaf(f, s[g * D + d], acc);
+  const int unit = p.split[2 * i];
+  const int h = unit % p.heads, sb = unit / p.heads, set = sb / p.batch, b = sb - set * p.batch;
+  const int first = sets.first[set], rows = (sets.first[set + 1] - first) * p.group;
+  if (row >= rows) return;
+  const int64_t stride = (int64_t)p.rows * (D + 2);
+  float top = -INFINITY, sum = 0.f, acc = 0.f;
+#pragma unroll 4
+  for (int k = slice; k <= more; k += SLICES) {
+    const float* s = p.part + (k == 0 ? 2 * i + 1 : 2 * (i + k)) * stride;
+    const float m = s[p.rows * D + row], l = s[p.rows * (D + 1) + row], a = s[row * D + d];
+    const float high = fmaxf(top, m), base = high == -INFINITY ? 0.f : high;
+    const float f = exp2_fast(top - base), g = exp2_fast(m - base);
+    sum = fmaf(g, l, f * sum);
+    acc = fmaf(g, a, f * acc);
+    top = high;
   }
+  if (d == 0) {
+    st[slice] = top;
+    sl[slice] = sum;
+  }
+  sa[slice][d] = acc;
+  __syncthreads();
+  if (slice != 0) return;
+#pragma unroll
+  for (int k = 1; k < SLICES; ++k) top = fmaxf(top, st[k]);
+  const float base = top == -INFINITY ? 0.f : top;
+  sum = acc = 0.f;
+#pragma unroll
+  for (int k = 0; k < SLICES; ++k) {
+    const float f = exp2_fast(st[k] - base);
+    sum = fmaf(f, sl[k], sum);
+    acc = fmaf(f, sa[k][d], acc);
+  }
+  const int mem = row / p.group, li = sets.member[first + mem];
+  const int64_t to = (((int64_t)li * p.batch + b) * p.heads + h) * p.group + row - mem * p.group;
   const float y = sum == 0.f ? 0.f : acc / sum;
-  p.out[(unit * p.group + g) * D + d] = (uint16_t)(M::pack(y, y) & 0xffffu);
-  if (d == 0 && p.lse)
-    p.lse[unit * p.group + g] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+  p.out[to * D + d] = (uint16_t)(M::pack(y, y) & 0xffffu);
+  if (d == 0 && p.lse) p.lse[to] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
-size_t work_bytes_of(int group, int D) {
-  return sizeof(float) * 2 * (size_t)kWorkers * group * (D + 2) + sizeof(int32_t) * 2 * kWorkers;
+size_t work_bytes_of(int D) {
+  return sizeof(float) * 2 * (size_t)kMaxWorkers * kMaxRows * (D + 2) + sizeof(int32_t) * 2 * kMaxWorkers;
 }
 
 template <int D, int FMT, int MODE>
-loopkv_status launch_decode_mode(const PagedDecodeParams& p, const Cells& cells, cudaStream_t stream) {
-  constexpr int rows = MODE == 2 ? 16 : 8;
-  const size_t smem = sizeof(float) * ((size_t)kWarps * rows * (D + 4) + (3 * kWarps + 2) * kMaxGroup) +
+loopkv_status launch_decode_mode(PagedDecodeParams p, const Sets& sets, cudaStream_t stream) {
+  using S = Shape<D, FMT, MODE>;
+  p.workers = S::kWorkers;
+  const size_t smem = kWarps * S::kWarpBytes + sizeof(float) * (3 * kWarps + 2) * kMaxRows +
                       sizeof(int) * ((size_t)p.batch + 1);
   const auto kernel = paged_decode_kernel<D, FMT, MODE>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return LOOPKV_ERR_CUDA;
-  kernel<<<p.workers, kThreads, smem, stream>>>(p, cells);
+  kernel<<<p.workers, kThreads, smem, stream>>>(p, sets);
   if (cudaGetLastError() != cudaSuccess) return LOOPKV_ERR_CUDA;
-  paged_join_kernel<D, FMT><<<dim3(p.workers, p.group), D, 0, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? LOOPKV_OK : LOOPKV_ERR_CUDA;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)p.workers, (unsigned)p.rows, 1);
+  cfg.blockDim = dim3(kJoinThreads, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, FMT>, p, sets) == cudaSuccess ? LOOPKV_OK : LOOPKV_ERR_CUDA;
 }
 
 template <int D, int FMT>
-loopkv_status launch_decode_format(const PagedDecodeParams& p, const Cells& cells, cudaStream_t stream) {
-  if (p.group <= 4) return launch_decode_mode<D, FMT, 0>(p, cells, stream);
-  if (p.group <= 8) return launch_decode_mode<D, FMT, 1>(p, cells, stream);
-  return launch_decode_mode<D, FMT, 2>(p, cells, stream);
+loopkv_status launch_decode_format(const PagedDecodeParams& p, const Sets& sets, cudaStream_t stream) {
+  if (p.rows <= 4) return launch_decode_mode<D, FMT, 0>(p, sets, stream);
+  if (p.rows <= 8) return launch_decode_mode<D, FMT, 1>(p, sets, stream);
+  return launch_decode_mode<D, FMT, 2>(p, sets, stream);
 }
 
 template <int D>
-loopkv_status launch_decode_dim(int format, const PagedDecodeParams& p, const Cells& cells,
+loopkv_status launch_decode_dim(int format, const PagedDecodeParams& p, const Sets& sets,
                                 cudaStream_t stream) {
   switch (format) {
-    case LOOPKV_PAGE_BF16: return launch_decode_format<D, LOOPKV_PAGE_BF16>(p, cells, stream);
-    case LOOPKV_PAGE_F16: return launch_decode_format<D, LOOPKV_PAGE_F16>(p, cells, stream);
-    default: return launch_decode_format<D, LOOPKV_PAGE_Q8>(p, cells, stream);
+    case LOOPKV_PAGE_BF16: return launch_decode_format<D, LOOPKV_PAGE_BF16>(p, sets, stream);
+    case LOOPKV_PAGE_F16: return launch_decode_format<D, LOOPKV_PAGE_F16>(p, sets, stream);
+    default: return launch_decode_format<D, LOOPKV_PAGE_Q8>(p, sets, stream);
   }
 }
 
@@ -679,7 +773,7 @@ using namespace loopkv;
 extern "C" loopkv_status loopkv_paged_workspace(const loopkv_page_pool* pool,
                                                 const loopkv_paged_desc* desc, size_t* bytes) {
   if (bytes == nullptr || !pool_ok(pool) || !desc_ok(pool, desc)) return LOOPKV_ERR_INVALID_ARG;
-  *bytes = work_bytes_of(desc->q_per_kv, pool->head_dim);
+  *bytes = work_bytes_of(pool->head_dim);
   return LOOPKV_OK;
 }
 
@@ -698,16 +792,33 @@ extern "C" loopkv_status loopkv_paged_decode(const loopkv_page_pool* pool, const
   if (!aligned4(d_table) || !aligned4(d_len) || !aligned16(d_out) || !aligned4(d_lse) ||
       !aligned16(d_work) || !aligned4(d_status))
     return LOOPKV_ERR_INVALID_ARG;
-  if (work_bytes < work_bytes_of(desc->q_per_kv, pool->head_dim)) return LOOPKV_ERR_INVALID_ARG;
-  Cells cl{};
-  bool any_current = false;
-  for (int i = 0; i < n_cells; ++i) {
-    if (h_cells[i] < 0 || h_cells[i] >= pool->n_cells) return LOOPKV_ERR_INVALID_ARG;
-    const bool cur = h_current != nullptr && h_current[i] != 0;
-    cl.cell[i] = h_cells[i] | (cur ? kCurrentBit : 0);
-    any_current = any_current || cur;
-  }
+  if (work_bytes < work_bytes_of(pool->head_dim)) return LOOPKV_ERR_INVALID_ARG;
+  // Listed cells that read the same tokens are sets: their pages are read once.
   if (pool->n_cells >= kCurrentBit) return LOOPKV_ERR_INVALID_ARG;
+  Sets sets{};
+  const int most = kMaxRows / desc->q_per_kv;  // members of a set
+  int n_sets = 0, largest = 0, place = 0;
+  bool any_current = false, taken[LOOPKV_MAX_CELLS_PER_CALL] = {};
+  auto key = [&](int i) { return h_cells[i] | (h_current != nullptr && h_current[i] != 0 ? kCurrentBit : 0); };
+  for (int i = 0; i < n_cells; ++i)
+    if (h_cells[i] < 0 || h_cells[i] >= pool->n_cells) return LOOPKV_ERR_INVALID_ARG;
+  for (int i = 0; i < n_cells; ++i) {
+    if (taken[i]) continue;
+    const int cell = key(i);
+    int size = 0;
+    sets.cell[n_sets] = cell;
+    sets.first[n_sets] = (uint16_t)place;
+    for (int j = i; j < n_cells && size < most; ++j) {
+      if (taken[j] || key(j) != cell) continue;
+      taken[j] = true;
+      sets.member[place++] = (uint16_t)j;
+      ++size;
+    }
+    ++n_sets;
+    largest = std::max(largest, size);
+    any_current = any_current || (cell & kCurrentBit) != 0;
+  }
+  sets.first[n_sets] = (uint16_t)place;
   if (any_current && (!rows_ok(cur_k) || !rows_ok(cur_v))) return LOOPKV_ERR_INVALID_ARG;
   // units are numbered in 32 bits
   if ((int64_t)n_cells * desc->batch * pool->n_kv_heads >= (1LL << 31)) return LOOPKV_ERR_INVALID_ARG;
@@ -725,20 +836,20 @@ extern "C" loopkv_status loopkv_paged_decode(const loopkv_page_pool* pool, const
   p.out = static_cast<uint16_t*>(d_out);
   p.lse = d_lse;
   p.part = static_cast<float*>(d_work);
-  p.split = reinterpret_cast<int32_t*>(p.part + 2 * (size_t)kWorkers * desc->q_per_kv * (pool->head_dim + 2));
+  p.split = reinterpret_cast<int32_t*>(p.part + 2 * (size_t)kMaxWorkers * kMaxRows * (pool->head_dim + 2));
   p.status = d_status;
-  p.n_cells = n_cells;
+  p.n_sets = n_sets;
+  p.rows = largest * desc->q_per_kv;
   p.batch = desc->batch;
   p.heads = pool->n_kv_heads;
   p.group = desc->q_per_kv;
   p.max_pages = desc->max_pages;
   p.n_pages = pool->n_pages;
-  p.workers = kWorkers;
   p.cell_rows = (int64_t)pool->n_pages * pool->n_kv_heads * pool->page_size;
   const float sm_scale = desc->sm_scale > 0.f ? desc->sm_scale : 1.0f / std::sqrt((float)pool->head_dim);
   p.scale2 = sm_scale * 1.4426950408889634f;
   p.div = PageDiv(pool->page_size);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return pool->head_dim == 64 ? launch_decode_dim<64>(pool->format, p, cl, s)
-                              : launch_decode_dim<128>(pool->format, p, cl, s);
+  return pool->head_dim == 64 ? launch_decode_dim<64>(pool->format, p, sets, s)
+                              : launch_decode_dim<128>(pool->format, p, sets, s);
 }
