@@ -66,7 +66,8 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kSms = 148;
 constexpr int kMaxWorkers = kSms * 4;
 constexpr int kTile = 16;            // tokens of a warp's step
-constexpr int kMinTiles = 2 * kWarps;  // tiles a worker takes at least
+constexpr int kMinCost = 2 * kWarps;  // cost a worker takes at least
+constexpr int kUnitCost = 6;          // tiles that a unit's start and end are worth
 constexpr int kMaxRows = LOOPKV_MAX_PAGED_GROUP;  // query rows of a set
 constexpr int kJoinThreads = 512;
 constexpr uint32_t kNoRow = 0xffffffffu;
@@ -243,7 +244,8 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
   const int v_piece = Q8 ? lane >> 4 : (lane >> 3) & 1;
   uint32_t status = 0;
 
-  // Tiles of every request (at least one: a unit without tokens is written too).
+  // Cost of a unit of every request: its tiles (at least one: a unit without
+  // tokens is written too) and its start and end.
   {
     const int per = (p.batch + kThreads - 1) / kThreads;
     int sum = 0;
@@ -255,7 +257,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
         status |= LOOPKV_PAGE_BAD_LENGTH;
         n = 0;
       }
-      const int t = max(1, (n + kTile - 1) / kTile);
+      const int t = kUnitCost + max(1, (n + kTile - 1) / kTile);
       prefix[b + 1] = t;
       sum += t;
     }
@@ -280,7 +282,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
   }
   const int per_request = p.n_sets * p.heads;
   const int64_t all = (int64_t)prefix[p.batch] * per_request;
-  const int64_t want = (all + kMinTiles - 1) / kMinTiles;
+  const int64_t want = (all + kMinCost - 1) / kMinCost;
   const int workers = (int)(want < p.workers ? want : p.workers);
   const int me = blockIdx.x;
   if (tid == 0) p.split[2 * me + 1] = 0;
@@ -298,17 +300,31 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
   }
 
   while (x < x1) {
-    const int tiles = prefix[b + 1] - prefix[b];
+    // position i of a unit's cost is its tile i - kUnitCost
+    const int cost = prefix[b + 1] - prefix[b], tiles = cost - kUnitCost;
     const int64_t rem = x - (int64_t)prefix[b] * per_request;
-    const int u = (int)(rem / tiles), t0 = (int)(rem - (int64_t)u * tiles);
+    const int u = (int)(rem / cost), from = (int)(rem - (int64_t)u * cost);
     const int set = u / p.heads, h = u - set * p.heads;
-    const int t1 = (int)min((int64_t)tiles, t0 + (x1 - x));
+    const int upto = (int)min((int64_t)cost, from + (x1 - x));
+    const int t0 = max(0, from - kUnitCost), t1 = upto - kUnitCost;
+    x += upto - from;
+    if (t1 <= 0) break;  // the share ends before the unit's first tile
     const int first = sets.first[set], rows = (sets.first[set + 1] - first) * p.group;
     int n = p.len[b];
     if (n < 0 || n > p.max_pages * p.div.size) n = 0;
     const bool current = (sets.cell[set] & kCurrentBit) != 0 && n > 0;
     const int64_t cell_row = (int64_t)(sets.cell[set] & ~kCurrentBit) * p.cell_rows + (int64_t)h * p.div.size;
     const int np = current ? n - 1 : n;  // tokens read from pages
+    if (n == 0) {
+      for (int i = tid; i < rows * (D / 8); i += kThreads) {
+        const int row = i / (D / 8), mem = row / p.group, li = sets.member[first + mem];
+        const int64_t at = (((int64_t)li * p.batch + b) * p.heads + h) * p.group + row - mem * p.group;
+        reinterpret_cast<uint4*>(p.out + at * D)[i - row * (D / 8)] = make_uint4(0, 0, 0, 0);
+        if (i == row * (D / 8) && p.lse) p.lse[at] = -INFINITY;
+      }
+      if (x == (int64_t)prefix[b + 1] * per_request) ++b;
+      continue;
+    }
 
     // The page of token (lane & 15) of a tile (-1: no such token), loaded a
     // step before its row is needed.
@@ -645,12 +661,11 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
     }
     if (!whole && t0 == 0 && tid == 0) {
       // the workers behind this one that hold the rest of the unit
-      const int64_t last = x + tiles - 1;
+      const int64_t last = x - upto + cost - 1;
       p.split[2 * me] = (set * p.batch + b) * p.heads + h;
       p.split[2 * me + 1] = (int)(((last + 1) * workers - 1) / all) - me;
     }
     __syncthreads();  // shared memory is free for the next unit
-    x += t1 - t0;
     if (x == (int64_t)prefix[b + 1] * per_request) ++b;
   }
   if (status && p.status) atomicOr(p.status, status);
