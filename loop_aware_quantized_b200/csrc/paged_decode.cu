@@ -70,7 +70,6 @@ constexpr int kMinCost = 2 * kWarps;  // cost a worker takes at least
 constexpr int kUnitCost = 6;          // tiles that a unit's start and end are worth
 constexpr int kMaxRows = LOOPKV_MAX_PAGED_GROUP;  // query rows of a set
 constexpr int kJoinThreads = 512;
-constexpr uint32_t kNoRow = 0xffffffffu;
 constexpr int kCurrentBit = 1 << 30;  // in a set's cell: the last token is in cur_k / cur_v
 
 struct RowView {
@@ -90,7 +89,8 @@ struct PagedDecodeParams {
   RowView q, cur_k, cur_v;
   uint16_t* out;
   float* lse;
-  float* part;        // [2 * workers][rows * (D + 2)] partial results: out, m, l
+  float* part;        // [2 * workers][rows][D] partial results
+  float2* stat;       // [2 * workers][rows] their maxima and sums
   int32_t* split;     // [workers][2]: a unit begun but not ended here, workers that continue it
   uint32_t* status;
   int32_t n_sets, batch, heads, group, max_pages, n_pages, workers;
@@ -130,6 +130,7 @@ struct Mma<LOOPKV_PAGE_BF16> {
   static __device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
   static __device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
   static constexpr float kShift = 0.f;
+  static constexpr float kSlack = 8.f;  // weights reach 2^8 before sums are rescaled
 };
 template <>
 struct Mma<LOOPKV_PAGE_Q8> : Mma<LOOPKV_PAGE_BF16> {};
@@ -159,6 +160,7 @@ struct Mma<LOOPKV_PAGE_F16> {
   // weights are exp2(s - m + 14): 2^14 at most, and only those below 2^-28
   // of the largest lose bits to fp16's smallest step
   static constexpr float kShift = 14.f;
+  static constexpr float kSlack = 0.f;  // 2^16 would be infinite
 };
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -215,7 +217,9 @@ struct Shape {
   static __device__ __forceinline__ int swizzle(int t) { return kPieces == 4 ? (t >> 1) & 3 : t & 7; }
 };
 
-template <int D, int FMT, int MODE>  // MODE 0: up to 4 query rows, 1: 8, 2: 16
+// MODE 0: up to 4 query rows, 1: 8, 2: 16.  FLAT: pages of whole tiles, so that
+// a tile's rows follow one another.
+template <int D, int FMT, int MODE, bool FLAT>
 __global__ void __launch_bounds__(kThreads, Shape<D, FMT, MODE>::kCtasPerSm)
 paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_constant__ Sets sets) {
   require_ieee_subnormals();
@@ -226,7 +230,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
   constexpr int ROWS = 8 * NT;               // query rows a warp keeps
   constexpr int OS = D + 4;                  // floats of a row in shared memory (banks)
   static_assert(ROWS * OS * 4 <= S::kWarpBytes, "a warp's results take the place of its tiles");
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(256) uint8_t smem[];
   float* const sm = reinterpret_cast<float*>(smem + kWarps * S::kWarpBytes);  // [kWarps + 1][kMaxRows] maxima
   float* const sl = sm + (kWarps + 1) * kMaxRows;                // sums
   float* const sz = sl + (kWarps + 1) * kMaxRows;                // [kWarps][kMaxRows] zero-point sums (Q8)
@@ -242,6 +246,10 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
   const int k_row = (lane & 7) + ((lane >> 4) << 3), k_piece = (lane >> 3) & 1;  // tokens 0-7 | 8-15 x 2 pieces
   const int v_row = (lane & 7) + (Q8 ? ((lane >> 3) & 1) << 3 : (lane >> 4) << 3);
   const int v_piece = Q8 ? lane >> 4 : (lane >> 3) & 1;
+  // (rows begin on multiples of their size, so a later piece is an exclusive or away)
+  const uint32_t k_at = k_row * S::kRowBytes + ((k_piece ^ S::swizzle(k_row)) << 4);
+  const uint32_t v_at = v_row * S::kRowBytes + ((v_piece ^ S::swizzle(v_row)) << 4);
+  const int64_t page_rows = (int64_t)p.heads * p.div.size;
   uint32_t status = 0;
 
   // Cost of a unit of every request: its tiles (at least one: a unit without
@@ -326,43 +334,51 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
       continue;
     }
 
-    // The page of token (lane & 15) of a tile (-1: no such token), loaded a
-    // step before its row is needed.
+    // The page of token (lane & 15) of a tile (FLAT: of its first token), loaded
+    // a step before the tile is copied.  A tile is then a row (FLAT: the first
+    // one; else the lane's token's) and a bit per token to be read.
     const int32_t* const entry = p.table + (int64_t)b * p.max_pages;
     auto page_of = [&](int tile) -> int {
-      const int pos = tile * kTile + (lane & 15);
+      const int pos = tile * kTile + (FLAT ? 0 : lane & 15);
       return tile < t1 && pos < np ? __ldg(entry + p.div.page(pos)) : INT_MIN;
     };
-    auto row_of = [&](int tile, int page) -> uint32_t {
-      if (page == INT_MIN) return kNoRow;
-      if (page < 0 || page >= p.n_pages) {
-        status |= LOOPKV_PAGE_BAD_PAGE;
-        return kNoRow;
-      }
-      const int pos = tile * kTile + (lane & 15), off = pos - p.div.page(pos) * p.div.size;
-      return (uint32_t)(cell_row + (int64_t)page * p.heads * p.div.size + off);
+    auto rows_of = [&](int tile, int page, uint32_t* row) -> uint32_t {
+      const int pos = tile * kTile + (FLAT ? 0 : lane & 15);
+      const bool good = page >= 0 && page < p.n_pages;
+      if (!good && page != INT_MIN) status |= LOOPKV_PAGE_BAD_PAGE;
+      *row = good ? (uint32_t)(cell_row + (int64_t)page * page_rows + (pos - p.div.page(pos) * p.div.size)) : 0u;
+      if (FLAT) return good ? (1u << min(kTile, np - pos)) - 1u : 0u;
+      return __ballot_sync(0xffffffffu, good) & 0xffffu;
     };
-    auto copy_rows = [&](uint32_t at, const uint8_t* src, uint32_t row) {
+    auto copy_rows = [&](uint32_t at, const uint8_t* src, uint32_t row, uint32_t bits) {
+      at += copy_row * S::kRowBytes;
+      src += 16 * piece;
+      bits >>= copy_row;
+      if constexpr (FLAT) {
+        src += ((uint64_t)row + copy_row) * S::kRowBytes;
 #pragma unroll
-      for (int i = 0; i < S::kCopies; ++i) {
-        const int t = i * S::kRowsPerCopy + copy_row;
-        const uint32_t from = __shfl_sync(0xffffffffu, row, t);
-        const bool on = from != kNoRow;
-        copy16(at + t * S::kRowBytes + ((piece ^ S::swizzle(t)) << 4),
-               src + (on ? (uint64_t)from * S::kRowBytes + 16 * piece : 0), on);
+        for (int i = 0; i < S::kCopies; ++i) {
+          const int t = i * S::kRowsPerCopy;
+          copy16(at + t * S::kRowBytes + ((piece ^ S::swizzle(t + copy_row)) << 4), src + t * S::kRowBytes, (bits >> t & 1) != 0);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < S::kCopies; ++i) {
+          const int t = i * S::kRowsPerCopy;
+          const uint32_t from = __shfl_sync(0xffffffffu, row, t + copy_row);
+          copy16(at + t * S::kRowBytes + ((piece ^ S::swizzle(t + copy_row)) << 4), src + (uint64_t)from * S::kRowBytes, (bits >> t & 1) != 0);
+        }
       }
     };
-    auto copy_keys = [&](int stage, uint32_t row) {
+    auto copy_keys = [&](int stage, uint32_t row, uint32_t bits) {
       const uint32_t at = ring_at + stage * S::kTileBytes;
-      copy_rows(at, p.k, row);
-      if (Q8 && lane < kTile) {
-        const bool on = row != kNoRow;
-        copy16(at + 2 * S::kRowsBytes + 16 * lane, reinterpret_cast<const uint8_t*>(p.meta) + (on ? (uint64_t)row * 16 : 0), on);
-      }
+      copy_rows(at, p.k, row, bits);
+      if (Q8 && lane < kTile)
+        copy16(at + 2 * S::kRowsBytes + 16 * lane, reinterpret_cast<const uint8_t*>(p.meta + (row + (FLAT ? (uint64_t)lane : 0))), (bits >> lane & 1) != 0);
       copy_commit();
     };
-    auto copy_values = [&](int stage, uint32_t row) {
-      copy_rows(ring_at + stage * S::kTileBytes + S::kRowsBytes, p.v, row);
+    auto copy_values = [&](int stage, uint32_t row, uint32_t bits) {
+      copy_rows(ring_at + stage * S::kTileBytes + S::kRowsBytes, p.v, row, bits);
       copy_commit();
     };
 
@@ -376,10 +392,11 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
       next_page = page_of(t0 + warp + S::kStages * kWarps);
 #pragma unroll
       for (int s = 0; s < S::kStages; ++s) {
-        const uint32_t row = row_of(t0 + warp + s * kWarps, pages[s]);
-        copy_keys(s, row);
-        copy_values(s, row);
-        valid |= (uint64_t)(__ballot_sync(0xffffffffu, row != kNoRow) & 0xffffu) << (16 * s);
+        uint32_t row;
+        const uint32_t bits = rows_of(t0 + warp + s * kWarps, pages[s], &row);
+        copy_keys(s, row, bits);
+        copy_values(s, row, bits);
+        valid |= (uint64_t)bits << (16 * s);
       }
     }
 
@@ -455,7 +472,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
 #pragma unroll
       for (int i = 0; i < S::kPieces / 2; ++i) {
         uint32_t w[4];  // tokens 0-7: pieces 2 i, 2 i + 1; tokens 8-15: the same
-        ldsm(w, keys + k_row * S::kRowBytes + (((2 * i + k_piece) ^ S::swizzle(k_row)) << 4));
+        ldsm(w, (keys + k_at) ^ (i << 5));
         if constexpr (Q8) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
@@ -477,10 +494,11 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
       const bool on[2][2] = {{(bits & 1) != 0, (bits & 2) != 0}, {(bits & 0x100) != 0, (bits & 0x200) != 0}};
       __syncwarp();
       const int ahead = tile + S::kStages * kWarps;
-      const uint32_t row = row_of(ahead, next_page);
+      uint32_t row;
+      const uint32_t ahead_bits = rows_of(ahead, next_page, &row);
       next_page = page_of(ahead + kWarps);
-      copy_keys(stage, row);
-      valid = valid >> 16 | (uint64_t)(__ballot_sync(0xffffffffu, row != kNoRow) & 0xffffu) << (16 * (S::kStages - 1));
+      copy_keys(stage, row, ahead_bits);
+      valid = valid >> 16 | (uint64_t)ahead_bits << (16 * (S::kStages - 1));
 
       // Weights, 4 tokens of a query row per lane.
       uint32_t ph[NT][2], pl[NT][2];
@@ -503,7 +521,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const float high = fmaxf(m[half], top - M::kShift);
-        if (__any_sync(0xffffffffu, high > m[half])) {
+        if (__any_sync(0xffffffffu, high > m[half] + M::kSlack)) {
           // a first maximum scales sums that are still zero
           const float a = m[half] == -INFINITY ? 0.f : exp2_fast(m[half] - high);
           m[half] = high;
@@ -543,7 +561,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
 #pragma unroll
       for (int i = 0; i < S::kPieces / 2; ++i) {
         uint32_t w[4];
-        ldsm_trans(w, values + v_row * S::kRowBytes + (((2 * i + v_piece) ^ S::swizzle(v_row)) << 4));
+        ldsm_trans(w, (values + v_at) ^ (i << 5));
         if constexpr (!Q8) {
           // tile i: rows r, r + 8 are channels 16 i + r, 16 i + 8 + r
 #pragma unroll
@@ -568,7 +586,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
         }
       }
       __syncwarp();
-      copy_values(stage, row);
+      copy_values(stage, row, ahead_bits);
       stage = stage + 1 == S::kStages ? 0 : stage + 1;
     }
     copy_wait<0>();  // empty groups only
@@ -622,30 +640,46 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
       }
     }
     __syncthreads();
+    if (tid < rows) {
+      // factors of the warps' sums in the place of their maxima; the joint
+      // maximum and sum in sl[i], sl[kMaxRows + i]
+      float top = with_current ? sm[kWarps * kMaxRows + tid] : -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[w * kMaxRows + tid]);
+      const float base = top == -INFINITY ? 0.f : top;
+      float sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = exp2_fast(sm[w * kMaxRows + tid] - base);
+        sum = fmaf(f, sl[w * kMaxRows + tid], sum);
+        sm[w * kMaxRows + tid] = f;
+      }
+      if (with_current) {
+        const float f = exp2_fast(sm[kWarps * kMaxRows + tid] - base);
+        sum += f;
+        sm[kWarps * kMaxRows + tid] = f;
+      }
+      sl[tid] = top;
+      sl[kMaxRows + tid] = sum;
+    }
+    __syncthreads();
     const bool whole = t0 == 0 && t1 == tiles;
-    float* const part = p.part + (int64_t)(2 * me + (t0 == 0 ? 1 : 0)) * p.rows * (D + 2);
+    const int slot = 2 * me + (t0 == 0 ? 1 : 0);
+    float* const part = p.part + (int64_t)slot * p.rows * D;
     for (int idx = tid; idx < rows * D; idx += kThreads) {
       const int i = idx / D, d = idx - i * D;
       const int mem = i / p.group, li = sets.member[first + mem];
-      float top = with_current ? sm[kWarps * kMaxRows + i] : -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[w * kMaxRows + i]);
-      const float base = top == -INFINITY ? 0.f : top;
-      float sum = 0.f, acc = 0.f;
+      float acc = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float f = exp2_fast(sm[w * kMaxRows + i] - base);
-        sum = fmaf(f, sl[w * kMaxRows + i], sum);
+        const float f = sm[w * kMaxRows + i];
         float y = so_of(w)[i * OS + d];
         if constexpr (MODE == 0) y += so_of(w)[(i + 4) * OS + d];
         if constexpr (Q8) y += sz[w * kMaxRows + i];
         acc = fmaf(f, y, acc);
       }
-      if (with_current) {
-        const float f = exp2_fast(sm[kWarps * kMaxRows + i] - base);
-        sum += f;
-        acc = fmaf(f, M::lo(p.cur_v.at(li, b, h)[d]), acc);
-      }
+      if (with_current) acc = fmaf(sm[kWarps * kMaxRows + i], M::lo(p.cur_v.at(li, b, h)[d]), acc);
+      const float top = sl[i], sum = sl[kMaxRows + i];
       if (whole) {
         const int64_t to = (((int64_t)li * p.batch + b) * p.heads + h) * p.group + i - mem * p.group;
         const float y = sum == 0.f ? 0.f : acc / sum;
@@ -653,10 +687,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
         if (d == 0 && p.lse) p.lse[to] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
       } else {
         part[idx] = acc;
-        if (d == 0) {
-          part[p.rows * D + i] = top;
-          part[p.rows * (D + 1) + i] = sum;
-        }
+        if (d == 0) p.stat[slot * p.rows + i] = make_float2(top, sum);
       }
     }
     if (!whole && t0 == 0 && tid == 0) {
@@ -673,16 +704,20 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
 
 // Join the parts of a unit that worker blockIdx.x began and did not end:
 // its own (slot 2 i + 1) and those of the workers behind it (slots 2 (i + k)).
-// A block does one query row, its threads the channels and kJoinThreads / D
-// interleaved shares of the parts.  Launched while the decode still runs
-// (every block waits for its end before it reads).
+// A block does one query row: all parts' maxima and sums at once, then their
+// channels, four to a thread, the parts dealt to groups of D / 4 threads, and
+// the groups' sums.  Launched while the decode still runs (every block waits
+// for its end before it reads).  What bounds it: four dependent round trips to
+// L2; with one thread a channel and a running maximum over the parts, two
+// units of 300 parts took 17 us.
 template <int D, int FMT>
 __global__ void __launch_bounds__(kJoinThreads)
 paged_join_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_constant__ Sets sets) {
   using M = Mma<FMT>;
-  constexpr int SLICES = kJoinThreads / D;
-  __shared__ float st[SLICES], sl[SLICES], sa[SLICES][D];
-  const int i = blockIdx.x, row = blockIdx.y, d = threadIdx.x % D, slice = threadIdx.x / D;
+  constexpr int WARPS = kJoinThreads / 32, GROUPS = kJoinThreads / (D / 4);
+  __shared__ float factor[kMaxWorkers], wm[WARPS], wl[WARPS];
+  __shared__ float4 sa[GROUPS][D / 4];
+  const int i = blockIdx.x, row = blockIdx.y, tid = threadIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int more = p.split[2 * i + 1];
   if (more == 0) return;
@@ -690,35 +725,55 @@ paged_join_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_cons
   const int h = unit % p.heads, sb = unit / p.heads, set = sb / p.batch, b = sb - set * p.batch;
   const int first = sets.first[set], rows = (sets.first[set + 1] - first) * p.group;
   if (row >= rows) return;
-  const int64_t stride = (int64_t)p.rows * (D + 2);
-  float top = -INFINITY, sum = 0.f, acc = 0.f;
-#pragma unroll 4
-  for (int k = slice; k <= more; k += SLICES) {
-    const float* s = p.part + (k == 0 ? 2 * i + 1 : 2 * (i + k)) * stride;
-    const float m = s[p.rows * D + row], l = s[p.rows * (D + 1) + row], a = s[row * D + d];
-    const float high = fmaxf(top, m), base = high == -INFINITY ? 0.f : high;
-    const float f = exp2_fast(top - base), g = exp2_fast(m - base);
-    sum = fmaf(g, l, f * sum);
-    acc = fmaf(g, a, f * acc);
-    top = high;
+  auto slot = [&](int k) { return k == 0 ? 2 * i + 1 : 2 * (i + k); };
+  constexpr int PER = (kMaxWorkers + kJoinThreads - 1) / kJoinThreads;
+  float2 mine[PER];
+  float top = -INFINITY, sum = 0.f;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const int k = tid + j * kJoinThreads;
+    mine[j] = k <= more ? p.stat[slot(k) * p.rows + row] : make_float2(-INFINITY, 0.f);
+    top = fmaxf(top, mine[j].x);
   }
-  if (d == 0) {
-    st[slice] = top;
-    sl[slice] = sum;
-  }
-  sa[slice][d] = acc;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if ((tid & 31) == 0) wm[tid >> 5] = top;
   __syncthreads();
-  if (slice != 0) return;
 #pragma unroll
-  for (int k = 1; k < SLICES; ++k) top = fmaxf(top, st[k]);
+  for (int w = 0; w < WARPS; ++w) top = fmaxf(top, wm[w]);
   const float base = top == -INFINITY ? 0.f : top;
-  sum = acc = 0.f;
 #pragma unroll
-  for (int k = 0; k < SLICES; ++k) {
-    const float f = exp2_fast(st[k] - base);
-    sum = fmaf(f, sl[k], sum);
-    acc = fmaf(f, sa[k][d], acc);
+  for (int j = 0; j < PER; ++j) {
+    const int k = tid + j * kJoinThreads;
+    const float f = exp2_fast(mine[j].x - base);
+    if (k <= more) factor[k] = f;
+    sum = fmaf(f, mine[j].y, sum);
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if ((tid & 31) == 0) wl[tid >> 5] = sum;
+  __syncthreads();
+  const int lane4 = tid % (D / 4), group = tid / (D / 4);
+  float4 acc4 = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int k = group; k <= more; k += GROUPS) {
+    const float4 a = reinterpret_cast<const float4*>(p.part + ((int64_t)slot(k) * p.rows + row) * D)[lane4];
+    const float f = factor[k];
+    acc4.x = fmaf(f, a.x, acc4.x);
+    acc4.y = fmaf(f, a.y, acc4.y);
+    acc4.z = fmaf(f, a.z, acc4.z);
+    acc4.w = fmaf(f, a.w, acc4.w);
+  }
+  sa[group][lane4] = acc4;
+  __syncthreads();
+  if (tid >= D) return;
+  const int d = tid;
+  float acc = 0.f;
+  sum = 0.f;
+#pragma unroll
+  for (int g = 0; g < GROUPS; ++g) acc += reinterpret_cast<const float*>(sa[g])[d];
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) sum += wl[w];
   const int mem = row / p.group, li = sets.member[first + mem];
   const int64_t to = (((int64_t)li * p.batch + b) * p.heads + h) * p.group + row - mem * p.group;
   const float y = sum == 0.f ? 0.f : acc / sum;
@@ -727,16 +782,16 @@ paged_join_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_cons
 }
 
 size_t work_bytes_of(int D) {
-  return sizeof(float) * 2 * (size_t)kMaxWorkers * kMaxRows * (D + 2) + sizeof(int32_t) * 2 * kMaxWorkers;
+  return sizeof(float) * 2 * (size_t)kMaxWorkers * kMaxRows * (D + 2) + sizeof(int32_t) * 2 * kMaxWorkers;  // part, stat, split
 }
 
-template <int D, int FMT, int MODE>
-loopkv_status launch_decode_mode(PagedDecodeParams p, const Sets& sets, cudaStream_t stream) {
+template <int D, int FMT, int MODE, bool FLAT>
+loopkv_status launch_decode_kernel(PagedDecodeParams p, const Sets& sets, cudaStream_t stream) {
   using S = Shape<D, FMT, MODE>;
   p.workers = S::kWorkers;
   const size_t smem = kWarps * S::kWarpBytes + sizeof(float) * (3 * kWarps + 2) * kMaxRows +
                       sizeof(int) * ((size_t)p.batch + 1);
-  const auto kernel = paged_decode_kernel<D, FMT, MODE>;
+  const auto kernel = paged_decode_kernel<D, FMT, MODE, FLAT>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return LOOPKV_ERR_CUDA;
   kernel<<<p.workers, kThreads, smem, stream>>>(p, sets);
@@ -751,6 +806,12 @@ loopkv_status launch_decode_mode(PagedDecodeParams p, const Sets& sets, cudaStre
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, FMT>, p, sets) == cudaSuccess ? LOOPKV_OK : LOOPKV_ERR_CUDA;
+}
+
+template <int D, int FMT, int MODE>
+loopkv_status launch_decode_mode(const PagedDecodeParams& p, const Sets& sets, cudaStream_t stream) {
+  return p.div.size % kTile == 0 ? launch_decode_kernel<D, FMT, MODE, true>(p, sets, stream)
+                                 : launch_decode_kernel<D, FMT, MODE, false>(p, sets, stream);
 }
 
 template <int D, int FMT>
@@ -851,7 +912,8 @@ extern "C" loopkv_status loopkv_paged_decode(const loopkv_page_pool* pool, const
   p.out = static_cast<uint16_t*>(d_out);
   p.lse = d_lse;
   p.part = static_cast<float*>(d_work);
-  p.split = reinterpret_cast<int32_t*>(p.part + 2 * (size_t)kMaxWorkers * kMaxRows * (pool->head_dim + 2));
+  p.stat = reinterpret_cast<float2*>(p.part + 2 * (size_t)kMaxWorkers * kMaxRows * pool->head_dim);
+  p.split = reinterpret_cast<int32_t*>(p.stat + 2 * (size_t)kMaxWorkers * kMaxRows);
   p.status = d_status;
   p.n_sets = n_sets;
   p.rows = largest * desc->q_per_kv;
