@@ -4,12 +4,15 @@
 // 4-bit cells' quantizer with 255 steps, in explicitly rounded fp32, so that
 // any IEEE implementation of the same steps gives the same codes).
 //
-// A thread moves 16 bytes of a key vector and the same 16 of the value
-// vector; the D / 8 threads of one (row, head) sit in one warp, so a Q8
-// vector's minimum and maximum are a few shuffles.  What bounds it: memory.
-// Each byte is read once and written once; a vector is 128 or 256
-// contiguous bytes on both sides.
+// A thread moves 16 bytes of a key vector and the same 16 of the value vector
+// (Q8: two such pieces of each, half a vector apart, so that what is done once
+// per vector is shared by more values); a vector's threads sit in one warp, so
+// its minimum and maximum are a few shuffles.  What bounds it: memory.  Each
+// byte is read once and written once; a vector is 128 or 256 contiguous bytes
+// on both sides.  A division per value took more than twice as long as the
+// bytes (2 cells of 16384 rows, 16 heads of 128: 175 us): see codes8.
 
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -47,42 +50,98 @@ __device__ __forceinline__ void unpack_bf16(const uint4& x, float (&f)[8]) {
   }
 }
 
-// The 8 codes of a thread's 8 values, given its vector's scale and minimum.
-__device__ __forceinline__ uint2 codes8(const float (&f)[8], float scale, float low) {
+__device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {  // low bytes
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+
+// By the definition, one value after another.
+__device__ __noinline__ uint2 codes8_exact(uint4 x, float scale, float low) {
+  float f[8];
+  unpack_bf16(x, f);
   uint32_t c[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int q = scale == 0.f ? 0 : __float2int_rn(__fdiv_rn(__fsub_rn(f[i], low), scale));
     c[i] = (uint32_t)(q < 0 ? 0 : (q > 255 ? 255 : q));
   }
-  return make_uint2(c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24,
-                    c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24);
+  return make_uint2(pack4(c[0], c[1], c[2], c[3]), pack4(c[4], c[5], c[6], c[7]));
+}
+
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  return (uint64_t)__float_as_uint(x) | (uint64_t)__float_as_uint(y) << 32;
+}
+
+// A vector's scale and minimum, and the reciprocal of the scale.
+struct Quantizer {
+  float scale, low, inverse;
+  __device__ __forceinline__ Quantizer(float mn, float mx) : low(mn) {
+    const float range = __fsub_rn(mx, mn);
+    scale = range == 0.f ? 0.f : __fdiv_rn(range, 255.f);
+    inverse = __frcp_rn(scale);
+  }
+  // no step of codes8 can overflow, or underflow where it matters (a quotient near a half)
+  __device__ __forceinline__ bool ordinary() const { return scale > 0x1p-100f && scale < 0x1p100f; }
+  __device__ __forceinline__ float zero() const { return low == 0.f ? 0.f : low; }  // a zero minimum is stored as +0
+};
+
+// The codes of 8 values: rne(fl(t / scale)), t = fl(x - low), two values to an
+// instruction.  Quotients on a half step are common (bf16 values are few bits
+// apart), so the rounded quotient itself is needed, and a division takes 10
+// instructions and more per value.  With y the rounded reciprocal of the
+// scale, the rounded quotient is q + y (t - q scale), fused, for any q within one
+// step of it (P. Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990).  t y is within 1.5 steps, and the same
+// correction once before brings it within one.  rne is the sum with 2^23; the
+// code is then the low byte.
+__device__ __forceinline__ uint2 codes8(const uint4& x, const Quantizer& z) {
+  if (!z.ordinary()) return codes8_exact(x, z.scale, z.low);
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  const uint64_t low = pair(-z.low, -z.low), y = pair(z.inverse, z.inverse), s = pair(-z.scale, -z.scale);
+  const uint64_t magic = pair(0x1p23f, 0x1p23f);
+  uint32_t c[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint64_t t = (uint64_t)(w[i] << 16) | (uint64_t)(w[i] & 0xffff0000u) << 32, q, r;
+    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(t) : "l"(low));
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(t), "l"(y));
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(q), "l"(s), "l"(t));
+      asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(q) : "l"(r), "l"(y));
+    }
+    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(q) : "l"(magic));
+    c[2 * i] = (uint32_t)q;
+    c[2 * i + 1] = (uint32_t)(q >> 32);
+  }
+  return make_uint2(pack4(c[0], c[1], c[2], c[3]), pack4(c[4], c[5], c[6], c[7]));
+}
+
+// The smallest and the negated largest of 16 bf16 values (two pieces), as a pair.
+__device__ __forceinline__ __nv_bfloat162 extremes(const uint4& x, const uint4& y) {
+  const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+  __nv_bfloat162 mn = *reinterpret_cast<const __nv_bfloat162*>(&w[0]), mx = mn;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) {
+    const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(&w[i]);
+    mn = __hmin2(mn, v);
+    mx = __hmax2(mx, v);
+  }
+  return __halves2bfloat162(__hmin(__low2bfloat16(mn), __high2bfloat16(mn)),
+                            __hneg(__hmax(__low2bfloat16(mx), __high2bfloat16(mx))));
 }
 
 template <int LANES>
-__device__ __forceinline__ void scale_zero(const float (&f)[8], float* scale, float* zero, float* low) {
-  float mn = f[0], mx = f[0];
+__device__ __forceinline__ Quantizer quantizer(__nv_bfloat162 e) {
 #pragma unroll
-  for (int i = 1; i < 8; ++i) {
-    mn = fminf(mn, f[i]);
-    mx = fmaxf(mx, f[i]);
-  }
-#pragma unroll
-  for (int o = LANES / 2; o > 0; o >>= 1) {
-    mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  }
-  const float range = __fsub_rn(mx, mn);
-  *scale = range == 0.f ? 0.f : __fdiv_rn(range, 255.f);
-  *low = mn;
-  *zero = mn == 0.f ? 0.f : mn;  // a zero minimum is stored as +0
+  for (int o = LANES / 2; o > 0; o >>= 1) e = __hmin2(e, __shfl_xor_sync(0xffffffffu, e, o));
+  return Quantizer(__low2float(e), -__high2float(e));
 }
 
 template <int D, bool Q8>
 __global__ void __launch_bounds__(kThreads)
 paged_append_kernel(const __grid_constant__ PagedAppendParams p, const __grid_constant__ CellList cells) {
   require_ieee_subnormals();
-  constexpr int LANES = D / 8;
+  constexpr int LANES = Q8 ? D / 16 : D / 8;
   const uint32_t i = blockIdx.x * (uint32_t)(kThreads / LANES) + threadIdx.x / LANES;
   const int part = threadIdx.x % LANES;
   const bool in = i < p.vectors;
@@ -92,29 +151,33 @@ paged_append_kernel(const __grid_constant__ PagedAppendParams p, const __grid_co
     if (p.status && part == 0) atomicOr(p.status, LOOPKV_PAGE_BAD_SLOT);
     slot = -1;
   }
-  uint4 k = make_uint4(0, 0, 0, 0), v = k;
   const int64_t ci = cells.out[blockIdx.y];
-  if (slot >= 0) {
-    k = *reinterpret_cast<const uint4*>(p.k + ci * p.k_cell + row * p.k_row + head * p.k_head + part * 8);
-    v = *reinterpret_cast<const uint4*>(p.v + ci * p.v_cell + row * p.v_row + head * p.v_head + part * 8);
-  }
+  const uint16_t* const ks = p.k + ci * p.k_cell + row * p.k_row + head * p.k_head + part * 8;
+  const uint16_t* const vs = p.v + ci * p.v_cell + row * p.v_row + head * p.v_head + part * 8;
   const int page = p.div.page(slot < 0 ? 0 : slot), off = slot - page * p.div.size;
   const int64_t at = cells.cell[blockIdx.y] * p.cell_rows +
                      ((int64_t)page * p.heads + head) * p.div.size + off;
   if constexpr (Q8) {
-    float kf[8], vf[8];
-    unpack_bf16(k, kf);
-    unpack_bf16(v, vf);
-    float4 m;
-    float kl, vl;
-    scale_zero<LANES>(kf, &m.x, &m.y, &kl);
-    scale_zero<LANES>(vf, &m.z, &m.w, &vl);
+    uint4 k[2], v[2];
+    k[0] = k[1] = v[0] = v[1] = make_uint4(0, 0, 0, 0);
+    if (slot >= 0) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        k[j] = *reinterpret_cast<const uint4*>(ks + j * (D / 2));
+        v[j] = *reinterpret_cast<const uint4*>(vs + j * (D / 2));
+      }
+    }
+    const Quantizer kz = quantizer<LANES>(extremes(k[0], k[1])), vz = quantizer<LANES>(extremes(v[0], v[1]));
     if (slot < 0) return;
-    *reinterpret_cast<uint2*>(p.kp + at * D + part * 8) = codes8(kf, m.x, kl);
-    *reinterpret_cast<uint2*>(p.vp + at * D + part * 8) = codes8(vf, m.z, vl);
-    if (part == 0) p.meta[at] = m;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      *reinterpret_cast<uint2*>(p.kp + at * D + part * 8 + j * (D / 2)) = codes8(k[j], kz);
+      *reinterpret_cast<uint2*>(p.vp + at * D + part * 8 + j * (D / 2)) = codes8(v[j], vz);
+    }
+    if (part == 0) p.meta[at] = make_float4(kz.scale, kz.zero(), vz.scale, vz.zero());
   } else {
     if (slot < 0) return;
+    const uint4 k = *reinterpret_cast<const uint4*>(ks), v = *reinterpret_cast<const uint4*>(vs);
     *reinterpret_cast<uint4*>(p.kp + (at * D + part * 8) * 2) = k;
     *reinterpret_cast<uint4*>(p.vp + (at * D + part * 8) * 2) = v;
   }
@@ -169,7 +232,8 @@ extern "C" loopkv_status loopkv_paged_append(const loopkv_page_pool* pool, const
     return LOOPKV_ERR_INVALID_ARG;
   if (stored == 0) return LOOPKV_OK;
   const int64_t vectors = (int64_t)n_rows * pool->n_kv_heads;
-  const int64_t blocks = (vectors * (pool->head_dim / 8) + kThreads - 1) / kThreads;
+  const bool q8 = pool->format == LOOPKV_PAGE_Q8;
+  const int64_t blocks = (vectors * (pool->head_dim / (q8 ? 16 : 8)) + kThreads - 1) / kThreads;
   if (vectors >= (1LL << 32) - kThreads || blocks >= (1LL << 31)) return LOOPKV_ERR_UNSUPPORTED;
   PagedAppendParams p{};
   p.k = static_cast<const uint16_t*>(k->data);
@@ -192,7 +256,6 @@ extern "C" loopkv_status loopkv_paged_append(const loopkv_page_pool* pool, const
   p.div = PageDiv(pool->page_size);
   const dim3 grid((unsigned)blocks, (unsigned)stored);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const bool q8 = pool->format == LOOPKV_PAGE_Q8;
   if (pool->head_dim == 64 && q8) paged_append_kernel<64, true><<<grid, kThreads, 0, s>>>(p, cl);
   else if (pool->head_dim == 64) paged_append_kernel<64, false><<<grid, kThreads, 0, s>>>(p, cl);
   else if (q8) paged_append_kernel<128, true><<<grid, kThreads, 0, s>>>(p, cl);

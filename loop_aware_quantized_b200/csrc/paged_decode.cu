@@ -67,7 +67,7 @@ constexpr int kSms = 148;
 constexpr int kMaxWorkers = kSms * 4;
 constexpr int kTile = 16;            // tokens of a warp's step
 constexpr int kMinCost = 2 * kWarps;  // cost a worker takes at least
-constexpr int kUnitCost = 6;          // tiles that a unit's start and end are worth
+constexpr int kUnitCost = 16;          // tiles that a unit's start and end are worth
 constexpr int kMaxRows = LOOPKV_MAX_PAGED_GROUP;  // query rows of a set
 constexpr int kJoinThreads = 512;
 constexpr int kCurrentBit = 1 << 30;  // in a set's cell: the last token is in cur_k / cur_v

@@ -9,16 +9,15 @@
 //                 thread of that row enters it in the table);
 //   page_release  pages i of the free list's new end: request b with
 //                 start_b <= i, its table entry.
-// One thread-block cluster does a whole call.  Every CTA reads the lengths
-// and does the (short) prefix sum for itself, so nothing but the cluster
-// barrier at the end joins them: behind it no CTA reads the lengths or the
-// free count any more and the first one stores the new ones, which is what
-// lets them be updated in place by one launch, and the call be captured and
-// replayed.  What bounds it: the launch and two dependent memory round trips
-// (lengths, then free list or table) for a decode step, the writes of a
-// cluster's SMs for long prompts.
+// Every CTA reads the lengths and does the (short) prefix sum for itself, so
+// CTAs need not wait for one another.  A short call is one CTA, which stores
+// the new lengths and free count behind a block barrier.  A long one is a grid
+// that expands, and one more CTA, launched while the grid runs, that repeats
+// the prefix sum, waits for the grid's end and stores them: behind that
+// nothing reads the old ones, which is what lets them be updated in place, and
+// the call be captured and replayed.  What bounds it: the launch and two
+// dependent memory round trips (lengths, then free list or table).
 
-#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -26,21 +25,20 @@
 
 #include "loopkv_internal.cuh"
 
-namespace cg = cooperative_groups;
-
 namespace loopkv {
 namespace {
 
 constexpr int kPageThreads = 1024;
-constexpr int kPageWarps = kPageThreads / 32;
+constexpr int kFewThreads = 256;  // of a short call of few requests
 constexpr int kPerThread = LOOPKV_MAX_PAGED_BATCH / kPageThreads;  // requests per thread at most
-constexpr int kChunk = 512;     // rows a warp expands with one search
-constexpr int kClusterRows = 4096;  // rows one CTA takes before a cluster of 8 does
+constexpr int kUnroll = 4;      // rows a lane looks up at a time
+constexpr int kSms = 148;
+constexpr int kShortWork = 4096;  // rows or pages of a one-CTA call
 constexpr long long kSatRows = 0x7fffffffLL;
 
 // Exclusive prefix sum over the block's threads; *total gets the sum.
 __device__ __forceinline__ long long block_scan(long long x, long long* warp_sums, long long* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   long long inc = x;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -51,16 +49,16 @@ __device__ __forceinline__ long long block_scan(long long x, long long* warp_sum
   if (lane == 31) warp_sums[warp] = inc;
   __syncthreads();
   if (warp == 0) {
-    long long s = warp_sums[lane];
+    long long s = lane < warps ? warp_sums[lane] : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, s, o);
       if (lane >= o) s += y;
     }
-    warp_sums[lane] = s;
+    if (lane < warps) warp_sums[lane] = s;
   }
   __syncthreads();
-  *total = warp_sums[kPageWarps - 1];
+  *total = warp_sums[warps - 1];
   return (warp == 0 ? 0 : warp_sums[warp - 1]) + inc - x;
 }
 
@@ -73,6 +71,19 @@ __device__ __forceinline__ int find_request(const int* start, int lo, int hi, in
   }
   return lo;
 }
+
+// The rows (or pages) of this warp: equal runs of whole warp widths.
+struct Run {
+  int begin, end;
+};
+__device__ __forceinline__ Run warp_run(int n) {
+  const int warps = (int)(gridDim.x * (blockDim.x >> 5)), warp = (int)(blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5));
+  const long long share = (((long long)n + warps - 1) / warps + 31) / 32 * 32;
+  const long long begin = warp * share, end = begin + share;
+  return {(int)(begin < n ? begin : n), (int)(end < n ? end : n)};
+}
+
+constexpr int kFirst = 1 << 30;  // a row at offset 0 of a new page: its table index instead of the offset
 
 struct PageParams {
   const int32_t* len;
@@ -87,6 +98,7 @@ struct PageParams {
   int32_t* free_count_out;
   uint32_t* status;
   int32_t batch, max_pages, n_pages, n_rows;
+  bool expand, finish;         // what this launch does: both, or one of them
   PageDiv div;
 };
 
@@ -107,9 +119,8 @@ __global__ void __launch_bounds__(kPageThreads) page_map_kernel(const __grid_con
   extern __shared__ int mem[];
   __shared__ long long warp_sums[32];
   const Shared sh = shared_arrays(mem, p.batch);
-  const cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
-  const int tid = threadIdx.x, per = (p.batch + kPageThreads - 1) / kPageThreads;
+  if (p.expand) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x, threads = blockDim.x, per = (p.batch + threads - 1) / threads;
   uint32_t status = 0;
 
   int len[kPerThread], add[kPerThread];
@@ -172,38 +183,55 @@ __global__ void __launch_bounds__(kPageThreads) page_map_kernel(const __grid_con
   if (tid == 0) sh.start[p.batch] = total;
   __syncthreads();
 
-  // Rows, in chunks of kChunk to a warp.
   const int lane = tid & 31;
-  const long long step = (long long)ranks * kPageWarps * kChunk;
-  for (long long r0 = ((long long)(tid >> 5) * ranks + rank) * kChunk; r0 < p.n_rows; r0 += step) {
-    const int r1 = (int)(r0 + kChunk < p.n_rows ? r0 + kChunk : p.n_rows);
-    const int lo = find_request(sh.start, 0, p.batch - 1, (int)r0);
-    const int hi = find_request(sh.start, lo, p.batch - 1, r1 - 1);
-    for (int r = (int)r0 + lane; r < r1; r += 32) {
-      int slot = -1;
-      if (r < total) {
-        const int b = find_request(sh.start, lo, hi, r);
-        const int n = sh.a[b];
-        if (n >= 0) {
-          const int pos = n + (r - sh.start[b]);
-          const int held = p.div.pages(n), j = p.div.page(pos), off = pos - j * p.div.size;
-          int32_t* entry = p.table + (size_t)b * p.max_pages + j;
-          const int page = j < held ? *entry : p.free[sh.b[b] - (j - held)];
-          const bool good = page >= 0 && page < p.n_pages;
-          if (j >= held && off == 0) *entry = good ? page : -1;
-          if (good) slot = page * p.div.size + off;
-          else status |= LOOPKV_PAGE_BAD_PAGE;
-          if (p.newest && r + 1 == sh.start[b + 1]) p.newest[b] = slot;
+  if (p.expand) {
+    // Rows, a contiguous run to every warp.
+    const Run run = warp_run(p.n_rows);
+    const int r0 = run.begin, r1 = run.end;
+    if (r0 < r1) {
+      const int lo = find_request(sh.start, 0, p.batch - 1, r0);
+      const int hi = find_request(sh.start, lo, p.batch - 1, r1 - 1);
+      for (int r = r0 + lane; r < r1; r += 32 * kUnroll) {
+        int b[kUnroll], page[kUnroll], off[kUnroll];
+        bool is_new[kUnroll];
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) {
+          const int row = r + 32 * k;
+          b[k] = -1;
+          if (row >= r1 || row >= total) continue;
+          const int req = find_request(sh.start, lo, hi, row);
+          const int n = sh.a[req];
+          if (n < 0) continue;
+          const int pos = n + (row - sh.start[req]);
+          const int held = p.div.pages(n), j = p.div.page(pos);
+          b[k] = req;
+          off[k] = pos - j * p.div.size;
+          is_new[k] = j >= held;
+          page[k] = is_new[k] ? p.free[sh.b[req] - (j - held)] : p.table[(size_t)req * p.max_pages + j];
+          if (is_new[k] && off[k] == 0) off[k] = j | kFirst;
+        }
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) {
+          const int row = r + 32 * k;
+          if (row >= r1) continue;
+          int slot = -1;
+          if (b[k] >= 0) {
+            const bool good = page[k] >= 0 && page[k] < p.n_pages, enter = (off[k] & kFirst) != 0;
+            if (enter) p.table[(size_t)b[k] * p.max_pages + (off[k] & ~kFirst)] = good ? page[k] : -1;
+            if (good) slot = page[k] * p.div.size + (enter ? 0 : off[k]);
+            else status |= LOOPKV_PAGE_BAD_PAGE;
+            if (p.newest && row + 1 == sh.start[b[k] + 1]) p.newest[b[k]] = slot;
+          }
+          if (p.slots) p.slots[row] = slot;
         }
       }
-      if (p.slots) p.slots[r] = slot;
     }
-  }
-  if (rank == 0) {
-    for (int b = tid; b <= p.batch; b += kPageThreads) {
-      p.starts[b] = sh.start[b];
-      // the other requests' newest slots come from the threads of their last rows
-      if (p.newest && b < p.batch && (sh.a[b] < 0 || sh.start[b] == sh.start[b + 1])) p.newest[b] = -1;
+    if (blockIdx.x == 0) {
+      for (int b = tid; b <= p.batch; b += threads) {
+        p.starts[b] = sh.start[b];
+        // the other requests' newest slots come from the threads of their last rows
+        if (p.newest && b < p.batch && (sh.a[b] < 0 || sh.start[b] == sh.start[b + 1])) p.newest[b] = -1;
+      }
     }
   }
   if (status && p.status) atomicOr(p.status, status);
@@ -212,9 +240,10 @@ __global__ void __launch_bounds__(kPageThreads) page_map_kernel(const __grid_con
     const long long y = __shfl_xor_sync(0xffffffffu, taken, o);
     taken = y > taken ? y : taken;
   }
+  if (!p.finish) return;
   if (lane == 0) warp_sums[tid >> 5] = taken;
-  cluster.sync();  // every CTA has read the lengths and the free count
-  if (rank != 0) return;
+  if (!p.expand) asm volatile("griddepcontrol.wait;" ::: "memory");
+  __syncthreads();  // every thread has read the lengths and the free count
 #pragma unroll
   for (int k = 0; k < kPerThread; ++k) {
     const int b = tid * per + k;
@@ -222,7 +251,7 @@ __global__ void __launch_bounds__(kPageThreads) page_map_kernel(const __grid_con
   }
   if (tid == 0) {
     long long most = 0;
-    for (int w = 0; w < kPageWarps; ++w) most = warp_sums[w] > most ? warp_sums[w] : most;
+    for (int w = 0; w < threads / 32; ++w) most = warp_sums[w] > most ? warp_sums[w] : most;
     *p.free_count_out = free_count - (int)most;
   }
 }
@@ -232,9 +261,8 @@ page_release_kernel(const __grid_constant__ PageParams p) {
   extern __shared__ int mem[];
   __shared__ long long warp_sums[32];
   const Shared sh = shared_arrays(mem, p.batch);
-  const cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
-  const int tid = threadIdx.x, per = (p.batch + kPageThreads - 1) / kPageThreads;
+  if (p.expand) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x, threads = blockDim.x, per = (p.batch + threads - 1) / threads;
   uint32_t status = 0;
 
   int len[kPerThread], cut[kPerThread], gone[kPerThread];
@@ -289,27 +317,39 @@ page_release_kernel(const __grid_constant__ PageParams p) {
   if (lane == 0) warp_sums[tid >> 5] = pushed;
   __syncthreads();
   long long most = 0;
-  for (int w = 0; w < kPageWarps; ++w) most = warp_sums[w] > most ? warp_sums[w] : most;
+  for (int w = 0; w < threads / 32; ++w) most = warp_sums[w] > most ? warp_sums[w] : most;
 
   const int total = (int)most;  // pages pushed: those of the admitted requests, a prefix
-  const long long step = (long long)ranks * kPageWarps * kChunk;
-  for (long long i0 = ((long long)(tid >> 5) * ranks + rank) * kChunk; i0 < total; i0 += step) {
-    const int i1 = (int)(i0 + kChunk < total ? i0 + kChunk : total);
-    const int lo = find_request(sh.start, 0, p.batch - 1, (int)i0);
-    const int hi = find_request(sh.start, lo, p.batch - 1, i1 - 1);
-    for (int i = (int)i0 + lane; i < i1; i += 32) {
-      const int b = find_request(sh.start, lo, hi, i);
-      int page = p.table[(size_t)b * p.max_pages + sh.a[b] + (i - sh.start[b])];
-      if (page < 0 || page >= p.n_pages) {
-        status |= LOOPKV_PAGE_BAD_PAGE;
-        page = -1;
+  if (p.expand) {
+    const Run run = warp_run(total);
+    const int i0 = run.begin, i1 = run.end;
+    if (i0 < i1) {
+      const int lo = find_request(sh.start, 0, p.batch - 1, i0);
+      const int hi = find_request(sh.start, lo, p.batch - 1, i1 - 1);
+      for (int i = i0 + lane; i < i1; i += 32 * kUnroll) {
+        int page[kUnroll];
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) {
+          const int at = i + 32 * k;
+          if (at >= i1) continue;
+          const int b = find_request(sh.start, lo, hi, at);
+          page[k] = p.table[(size_t)b * p.max_pages + sh.a[b] + (at - sh.start[b])];
+        }
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) {
+          const int at = i + 32 * k;
+          if (at >= i1) continue;
+          const bool good = page[k] >= 0 && page[k] < p.n_pages;
+          if (!good) status |= LOOPKV_PAGE_BAD_PAGE;
+          p.free[free_count + at] = good ? page[k] : -1;
+        }
       }
-      p.free[free_count + i] = page;
     }
   }
   if (status && p.status) atomicOr(p.status, status);
-  cluster.sync();  // every CTA has read the lengths and the free count
-  if (rank != 0) return;
+  if (!p.finish) return;
+  if (!p.expand) asm volatile("griddepcontrol.wait;" ::: "memory");
+  __syncthreads();  // every thread has read the lengths and the free count
 #pragma unroll
   for (int k = 0; k < kPerThread; ++k) {
     const int b = tid * per + k;
@@ -328,22 +368,32 @@ bool page_args_ok(int32_t batch, int32_t page_size, int32_t max_pages, int32_t n
 }
 
 // work: rows (map) or pages (release) the call may have to expand, at most.
+// A short call is one launch of one CTA: at 4096 rows that takes as long as the two
+// launches of a long one.
 template <typename Kernel>
-loopkv_status launch_pages(Kernel kernel, const PageParams& p, long long work, void* stream) {
+loopkv_status launch_pages(Kernel kernel, PageParams p, long long work, void* stream) {
   const size_t smem = sizeof(int) * (3 * (size_t)p.batch + 1);
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+  if (smem > 40 * 1024 &&  // 48 KB less the static part need no asking
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return LOOPKV_ERR_CUDA;
-  const unsigned ctas = work <= kClusterRows ? 1 : 8;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  p.expand = true;
+  p.finish = work <= kShortWork;
+  const int few = p.finish && work <= kUnroll * kFewThreads && p.batch <= kFewThreads;
+  const long long ctas = p.finish ? 1 : std::min<long long>((work + kPageThreads - 1) / kPageThreads, kSms);
+  kernel<<<(unsigned)ctas, few ? kFewThreads : kPageThreads, smem, s>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return LOOPKV_ERR_CUDA;
+  if (p.finish) return LOOPKV_OK;
+  p.expand = false;
+  p.finish = true;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(ctas, 1, 1);
+  cfg.gridDim = dim3(1, 1, 1);
   cfg.blockDim = dim3(kPageThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
-  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cfg.stream = s;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? LOOPKV_OK : LOOPKV_ERR_CUDA;

@@ -240,6 +240,56 @@ def test_paged_append(dev, fmt, cells, rows, heads, dim, ps):
             assert np.array_equal(as_bytes(g_), w), name
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+def test_paged_append_q8_codes_at_their_borders(dev, dim):
+    # quotients on and next to half steps, ranges from subnormal to huge: the codes of the
+    # definition, bit for bit
+    import torch
+    from loop_aware_quantized_b200 import paged_append
+    rng = np.random.default_rng(dim)
+    rows, heads = 600, 2
+    x = rng.standard_normal((2, rows, heads, dim))
+    x[:, :100] = rng.integers(-127, 128, (2, 100, heads, dim))
+    x[:, :100, :, 0], x[:, :100, :, 1] = -127.5, 127.5             # scale 1: halves everywhere
+    x[:, 100:200] = rng.integers(-20, 21, (2, 100, heads, dim)) / 2.0
+    x[:, 200:500] *= 10.0 ** rng.uniform(-38, 37, (2, 300, heads, 1))
+    x[:, 500:520] = rng.integers(-3, 4, (2, 20, heads, dim)) * 2.0 ** -133  # subnormal ranges
+    x[:, 520:540, :, 1:] = 0                                       # one value apart from the rest
+    x[:, 540:560] = np.where(rng.random((2, 20, heads, dim)) < 0.5, 0.0, -0.0)
+    x = torch.tensor(x, dtype=torch.float32, device=dev).to(torch.bfloat16)
+    ps = 16
+    kp, vp, meta = empty_pool(dev, "q8", (1, -(-rows // ps), heads, ps, dim))
+    paged_append([0], x[:1], x[1:], ints(np.arange(rows), dev), kp, vp, meta=meta)
+    flat = lambda t: host(t[0].transpose(1, 2).reshape(-1, heads, t.shape[-1])[:rows])  # noqa: E731
+    for part, (vec, pages) in enumerate(((x[0], kp), (x[1], vp))):
+        code, scale, zero = R.quantize(host(vec))
+        assert np.array_equal(flat(pages), code)
+        got = flat(meta)[..., 2 * part:2 * part + 2]
+        assert np.array_equal(got.view(np.uint32), np.stack([scale, zero], -1).view(np.uint32))
+
+
+def test_page_calls_around_the_one_block_limit(dev):
+    # rows (map) and pages (release) just below, at and above what one block takes
+    for rows in (1, 1023, 1024, 1025, 4095, 4096, 4097, 5000):
+        rng = np.random.default_rng(rows)
+        lengths = rng.integers(0, 30, 40)
+        new = np.bincount(rng.integers(0, 40, rows), minlength=40)
+        n_pages = int((-(-(lengths + new) // 4)).sum()) + 1
+        table, free, count = make_tables(rng, lengths, int((lengths + new).max()) // 4 + 1, 4, n_pages)
+        for in_place in (False, True):
+            check_map(dev, lengths, new, table, free, count, 4, rows, in_place)
+    from loop_aware_quantized_b200 import page_release
+    for n_pages in (4096, 4097, 9000):
+        rng = np.random.default_rng(n_pages)
+        lengths = rng.integers(0, n_pages // 64, 64)
+        table, free, count = make_tables(rng, lengths, n_pages, 1, n_pages)
+        new = np.where(rng.random(64) < 0.8, 0, lengths // 2)
+        t = [ints(x, dev) for x in (lengths, new, table, free, [count])]
+        page_release(*t, 1, lengths_out=t[1])            # the new lengths' own memory
+        f, n, c, st = R.page_release(lengths, new, table, free, count, 1)
+        assert np.array_equal(host(t[3]), f) and np.array_equal(host(t[1]), n) and int(t[4]) == c
+
+
 def test_paged_append_reads_strided_vectors(dev):
     import torch
     from loop_aware_quantized_b200 import paged_append
@@ -376,6 +426,29 @@ def test_decode_current_tokens(dev, fmt):
     c.check(with_cur=True)
     c.check(with_cur=True, current=[True, False, False, True])
     c.check()
+
+
+def test_decode_many_cells_of_one_pool_cell(dev):
+    # listed cells that read the same tokens, more query rows than one pass over the pages takes
+    for fmt, group, times in (("bf16", 1, 37), ("q8", 3, 11), ("fp16", 16, 3)):
+        cells = [1, 0] * (times // 2) + [1]
+        c = Case(dev, fmt, [33, 0, 700, 1], heads=2, group=group, dim=64, ps=24, cells=cells, seed=18)
+        c.check()
+        c.check(with_cur=True, current=[i % 3 > 0 for i in range(len(cells))])
+
+
+def test_decode_rising_maximum(dev):
+    # every tile's scores above the last one's, by little and by much
+    import torch
+    for fmt, step in (("bf16", 0.1), ("bf16", 3.0), ("fp16", 0.1), ("fp16", 3.0), ("bf16", -3.0)):
+        c = Case(dev, fmt, [1500], heads=1, group=2, dim=64, ps=16, seed=19)
+        c.q[:] = 0.25
+        ramp = torch.arange(1500, device=dev) // 16 * step
+        page = torch.tensor(c.table[0, :94], device=dev)
+        flat = torch.zeros(94 * 16, device=dev)
+        flat[:1500] = ramp
+        c.kp[0, page, 0] = flat.reshape(94, 16, 1).to(c.kp.dtype)
+        c.check()
 
 
 def test_decode_scale_and_sharp_scores(dev):
