@@ -15,9 +15,10 @@ _PAGED = ("PagedCache", "page_map", "page_release", "paged_append", "paged_decod
 
 def __getattr__(name):
     if name in _EXPORTS:
-        from . import loopkv
-        return getattr(loopkv, name)
-    if name in _PAGED:
-        from . import paged
-        return getattr(paged, name)
-    raise AttributeError(name)
+        from . import loopkv as module
+    elif name in _PAGED:
+        from . import paged as module
+    else:
+        raise AttributeError(name)
+    globals()[name] = value = getattr(module, name)  # found without this call from now on
+    return value

@@ -20,64 +20,63 @@ contiguous channels; their other strides are free (multiples of 8 elements), so
 slices of a fused projection's output can be given as they are.
 """
 
-import contextlib
 import ctypes
+import functools
 
 import numpy as np
+import torch
 
 from . import loopkv as _lk
 from .loopkv import _check, _invalid
 
-_FORMATS = None
+# Page dtype -> (format, dtype of the vectors)
+_FORMATS = {torch.bfloat16: (_lk.LOOPKV_PAGE_BF16, torch.bfloat16),
+            torch.float16: (_lk.LOOPKV_PAGE_F16, torch.float16),
+            torch.uint8: (_lk.LOOPKV_PAGE_Q8, torch.bfloat16)}
+_I32, _F32 = torch.int32, torch.float32
+
+# A decode step's calls are a few microseconds of device time each, so checks
+# are written for the case that they pass, with few attribute reads, and what
+# is wrong is found out afterwards.
 
 
-def _formats():
-    """Page dtype -> (format, dtype of the vectors)."""
-    global _FORMATS
-    if _FORMATS is None:
-        import torch
-        _FORMATS = {torch.bfloat16: (_lk.LOOPKV_PAGE_BF16, torch.bfloat16),
-                    torch.float16: (_lk.LOOPKV_PAGE_F16, torch.float16),
-                    torch.uint8: (_lk.LOOPKV_PAGE_Q8, torch.bfloat16)}
-    return _FORMATS
-
-
-_NOTHING = contextlib.nullcontext()
-
-
-def _place(where, device, stream):
-    """(context, stream handle) of a launch on ``device``: the stream given, or
-    the device's current one, with the device made current if it is not."""
-    import torch
+def _place(where, index, stream):
+    """(stream handle, context or None) of a launch on device ``index``: the
+    stream given, or the device's current one, with the device made current if
+    it is not."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-        if stream.device_index == torch.cuda.current_device():
-            return _NOTHING, stream.cuda_stream
-        return torch.cuda.device(device), stream.cuda_stream
-    if stream.device != device:
-        raise _invalid(where, "the stream is on %s, the tensors on %s" % (stream.device, device))
-    return torch.cuda.stream(stream), stream.cuda_stream
+        # the handle alone: a torch.cuda.Stream object takes 2 us to make
+        handle = torch._C._cuda_getCurrentRawStream(index)
+        return handle, None if torch.cuda.current_device() == index else torch.cuda.device(index)
+    if stream.device_index != index:
+        raise _invalid(where, "the stream is on %s, the tensors on cuda:%d" % (stream.device, index))
+    return stream.cuda_stream, torch.cuda.stream(stream)
 
 
-def _ints(t, where, name, device, shape):
-    """Pointer of a contiguous int32 tensor of a given shape."""
-    import torch
+def _wrong(t, where, name, dtype, index, shape):
+    """What a tensor argument that failed its check lacks."""
     if not isinstance(t, torch.Tensor):
-        raise _invalid(where, "%s must be a torch tensor, not %s" % (name, type(t).__name__))
-    if t.device != device or not t.is_cuda:
-        raise _invalid(where, "%s must be on %s, not %s" % (
-            name, device if device.type == "cuda" else "a CUDA device", t.device))
-    if t.dtype != torch.int32:
-        raise _invalid(where, "%s must be torch.int32, not %s" % (name, t.dtype))
-    if tuple(t.shape) != shape:
-        raise _invalid(where, "%s must have shape %s, not %s" % (name, shape, tuple(t.shape)))
-    if not t.is_contiguous():
-        raise _invalid(where, "%s must be contiguous" % name)
-    return t.data_ptr()
+        return _invalid(where, "%s must be a torch tensor, not %s" % (name, type(t).__name__))
+    if index < 0 or t.get_device() != index:
+        return _invalid(where, "%s must be on %s, not %s" % (
+            name, "a CUDA device" if index < 0 else "cuda:%d" % index, t.device))
+    if t.dtype != dtype:
+        return _invalid(where, "%s must be %s, not %s" % (name, dtype, t.dtype))
+    if tuple(t.shape) != tuple(shape):
+        return _invalid(where, "%s must have shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
+    return _invalid(where, "%s must be contiguous" % name)
 
 
-def _status(status, where, device):
-    return None if status is None else _ints(status, where, "status", device, (1,))
+def _full(t, where, name, dtype, index, shape):
+    """Pointer of a contiguous tensor of a given type and shape on a device."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and \
+            t.shape == shape and index >= 0 and t.is_contiguous():
+        return t.data_ptr()
+    raise _wrong(t, where, name, dtype, index, shape)
+
+
+def _ints(t, where, name, index, shape):
+    return _full(t, where, name, _I32, index, shape)
 
 
 def _size(value, where, name):
@@ -87,12 +86,22 @@ def _size(value, where, name):
 
 
 def _shape(t, where, name, ndim):
-    import torch
     if not isinstance(t, torch.Tensor):
         raise _invalid(where, "%s must be a torch tensor, not %s" % (name, type(t).__name__))
-    if t.dim() != ndim:
-        raise _invalid(where, "%s must have %d dimensions, not %d" % (name, ndim, t.dim()))
-    return tuple(t.shape)
+    shape = t.shape
+    if len(shape) != ndim:
+        raise _invalid(where, "%s must have %d dimensions, not %d" % (name, ndim, len(shape)))
+    return shape
+
+
+def _launch(fn, context, *args):
+    if context is None:
+        rc = fn(*args)
+    else:
+        with context:
+            rc = fn(*args)
+    if rc:
+        _check(rc, fn.__name__)
 
 
 def page_map(lengths, n_new, table, free, free_count, page_size, slots, starts, newest=None,
@@ -111,24 +120,21 @@ def page_map(lengths, n_new, table, free, free_count, page_size, slots, starts, 
     batch, width = _shape(table, where, "table", 2)
     (n_pages,), (rows,) = _shape(free, where, "free", 1), _shape(slots, where, "slots", 1)
     page_size = _size(page_size, where, "page_size")
-    dev = table.device
-    lengths_out = lengths if lengths_out is None else lengths_out
-    free_count_out = free_count if free_count_out is None else free_count_out
-    args = (_ints(lengths, where, "lengths", dev, (batch,)),
-            _ints(n_new, where, "n_new", dev, (batch,)),
-            _ints(table, where, "table", dev, (batch, width)),
-            _ints(free, where, "free", dev, (n_pages,)),
-            _ints(free_count, where, "free_count", dev, (1,)),
-            _ints(slots, where, "slots", dev, (rows,)),
-            _ints(starts, where, "starts", dev, (batch + 1,)),
-            None if newest is None else _ints(newest, where, "newest", dev, (batch,)),
-            _ints(lengths_out, where, "lengths_out", dev, (batch,)),
-            _ints(free_count_out, where, "free_count_out", dev, (1,)),
-            _status(status, where, dev))
-    context, handle = _place(where, dev, stream)
-    with context:
-        rc = _lk._lib.loopkv_page_map(batch, page_size, width, n_pages, rows, *args, handle)
-    _check(rc, "loopkv_page_map")
+    index, per_request, one = table.get_device(), (batch,), (1,)
+    d_len = _ints(lengths, where, "lengths", index, per_request)
+    d_count = _ints(free_count, where, "free_count", index, one)
+    d_new = _ints(n_new, where, "n_new", index, per_request)
+    d_table = _ints(table, where, "table", index, (batch, width))
+    d_free = _ints(free, where, "free", index, (n_pages,))
+    d_slots = _ints(slots, where, "slots", index, (rows,))
+    d_starts = _ints(starts, where, "starts", index, (batch + 1,))
+    d_newest = None if newest is None else _ints(newest, where, "newest", index, per_request)
+    d_len_out = d_len if lengths_out is None else _ints(lengths_out, where, "lengths_out", index, per_request)
+    d_count_out = d_count if free_count_out is None else _ints(free_count_out, where, "free_count_out", index, one)
+    d_status = None if status is None else _ints(status, where, "status", index, one)
+    handle, context = _place(where, index, stream)
+    _launch(_lk._lib.loopkv_page_map, context, batch, page_size, width, n_pages, rows, d_len, d_new, d_table,
+            d_free, d_count, d_slots, d_starts, d_newest, d_len_out, d_count_out, d_status, handle)
     return slots, starts
 
 
@@ -143,60 +149,49 @@ def page_release(lengths, new_lengths, table, free, free_count, page_size, lengt
     batch, width = _shape(table, where, "table", 2)
     (n_pages,) = _shape(free, where, "free", 1)
     page_size = _size(page_size, where, "page_size")
-    dev = table.device
-    lengths_out = lengths if lengths_out is None else lengths_out
-    free_count_out = free_count if free_count_out is None else free_count_out
-    args = (_ints(lengths, where, "lengths", dev, (batch,)),
-            _ints(new_lengths, where, "new_lengths", dev, (batch,)),
-            _ints(table, where, "table", dev, (batch, width)),
-            _ints(free, where, "free", dev, (n_pages,)),
-            _ints(free_count, where, "free_count", dev, (1,)),
-            _ints(lengths_out, where, "lengths_out", dev, (batch,)),
-            _ints(free_count_out, where, "free_count_out", dev, (1,)),
-            _status(status, where, dev))
-    context, handle = _place(where, dev, stream)
-    with context:
-        rc = _lk._lib.loopkv_page_release(batch, page_size, width, n_pages, *args, handle)
-    _check(rc, "loopkv_page_release")
+    index, per_request, one = table.get_device(), (batch,), (1,)
+    d_len = _ints(lengths, where, "lengths", index, per_request)
+    d_count = _ints(free_count, where, "free_count", index, one)
+    d_new = _ints(new_lengths, where, "new_lengths", index, per_request)
+    d_table = _ints(table, where, "table", index, (batch, width))
+    d_free = _ints(free, where, "free", index, (n_pages,))
+    d_len_out = d_len if lengths_out is None else _ints(lengths_out, where, "lengths_out", index, per_request)
+    d_count_out = d_count if free_count_out is None else _ints(free_count_out, where, "free_count_out", index, one)
+    d_status = None if status is None else _ints(status, where, "status", index, one)
+    handle, context = _place(where, index, stream)
+    _launch(_lk._lib.loopkv_page_release, context, batch, page_size, width, n_pages, d_len, d_new, d_table, d_free,
+            d_count, d_len_out, d_count_out, d_status, handle)
 
 
 def _pool(k_pages, v_pages, meta, where):
-    """(loopkv_page_pool, dtype of the vectors) of the page tensors."""
-    import torch
+    """(loopkv_page_pool, dtype of the vectors, device index) of the page tensors."""
     shape = _shape(k_pages, where, "k_pages", 5)
-    if k_pages.dtype not in _formats():
+    page_dtype, index = k_pages.dtype, k_pages.get_device()
+    if page_dtype not in _FORMATS:
         raise _invalid(where, "k_pages must be torch.bfloat16, torch.float16 or torch.uint8, not %s"
-                       % k_pages.dtype)
-    fmt, dtype = _formats()[k_pages.dtype]
-    dev = k_pages.device
-    if not k_pages.is_cuda or not k_pages.is_contiguous():
-        raise _invalid(where, "k_pages must be contiguous and on a CUDA device, not on %s" % dev)
-    _lk._need(v_pages, where, "v_pages", (k_pages.dtype,), shape=shape, device=dev)
+                       % page_dtype)
+    fmt, dtype = _FORMATS[page_dtype]
+    d_k = _full(k_pages, where, "k_pages", page_dtype, index, shape)
+    d_v = _full(v_pages, where, "v_pages", page_dtype, index, shape)
     if (meta is None) != (fmt != _lk.LOOPKV_PAGE_Q8):
         raise _invalid(where, "meta belongs to uint8 pages, and to no others")
-    if meta is not None:
-        _lk._need(meta, where, "meta", (torch.float32,), shape=shape[:4] + (4,), device=dev)
+    d_meta = None if meta is None else _full(meta, where, "meta", _F32, index, shape[:4] + (4,))
     cells, pages, heads, page_size, dim = shape
-    return _lk.loopkv_page_pool(cells, pages, page_size, heads, dim, fmt, k_pages.data_ptr(),
-                                v_pages.data_ptr(), None if meta is None else meta.data_ptr()), dtype
+    return _lk.loopkv_page_pool(cells, pages, page_size, heads, dim, fmt, d_k, d_v, d_meta), dtype, index
 
 
-def _rows(t, where, name, dtype, device, shape):
-    """loopkv_rows of a [cells, rows, heads, head dim] tensor."""
+def _rows(t, where, name, dtype, index, shape):
+    """loopkv_rows of a [cells, rows, heads, head dim] tensor (heads None: any)."""
     got = _shape(t, where, name, 4)
-    if t.device != device:
-        raise _invalid(where, "%s must be on %s, not %s" % (name, device, t.device))
-    if t.dtype != dtype:
-        raise _invalid(where, "%s must be %s, not %s" % (name, dtype, t.dtype))
-    if any(w is not None and w != g for w, g in zip(shape, got)):
-        raise _invalid(where, "%s has shape %s; expected (%s)" % (
-            name, got, ", ".join("any" if w is None else str(w) for w in shape)))
-    strides = t.stride()
-    outer = [0 if n <= 1 else s for n, s in zip(got[:3], strides[:3])]
-    if strides[3] != 1 or any(s & 7 for s in outer) or t.data_ptr() & 15:
+    if t.dtype is not dtype or t.get_device() != index or got[:2] != shape[:2] or got[3] != shape[3] or \
+            (got[2] != shape[2] and shape[2] is not None):
+        raise _wrong(t, where, name, dtype, index, tuple(g if w is None else w for w, g in zip(shape, got)))
+    strides, at = t.stride(), t.data_ptr()
+    cell, row, head = (0 if n <= 1 else s for n, s in zip(got, strides[:3]))
+    if strides[3] != 1 or (cell | row | head) & 7 or at & 15:
         raise _invalid(where, "%s must have contiguous channels, strides that are multiples of 8 "
                               "and start on a 16-byte boundary; its strides are %s" % (name, strides))
-    return _lk.loopkv_rows(t.data_ptr(), *outer)
+    return _lk.loopkv_rows(at, cell, row, head)
 
 
 def _cells(cells, where):
@@ -214,21 +209,29 @@ def paged_append(cells, k, v, slots, k_pages, v_pages, meta=None, status=None, s
     is stored of that input).  Rows with slot -1 are skipped.  uint8 pages get
     codes and ``meta`` their scales and zero points."""
     where = "paged_append"
-    pool, dtype = _pool(k_pages, v_pages, meta, where)
-    dev = k_pages.device
+    pool, dtype, index = _pool(k_pages, v_pages, meta, where)
     cells = _cells(cells, where)
     (rows,) = _shape(slots, where, "slots", 1)
     shape = (cells.size, rows, pool.n_kv_heads, pool.head_dim)
-    kr = _rows(k, where, "k", dtype, dev, shape)
-    vr = _rows(v, where, "v", dtype, dev, shape)
-    d_slots = _ints(slots, where, "slots", dev, (rows,))
-    d_status = _status(status, where, dev)
-    context, handle = _place(where, dev, stream)
-    with context:
-        rc = _lk._lib.loopkv_paged_append(
-            ctypes.addressof(pool), cells.ctypes.data, cells.size, rows, d_slots,
-            ctypes.addressof(kr), ctypes.addressof(vr), d_status, handle)
-    _check(rc, "loopkv_paged_append")
+    kr = _rows(k, where, "k", dtype, index, shape)
+    vr = _rows(v, where, "v", dtype, index, shape)
+    d_slots = _ints(slots, where, "slots", index, (rows,))
+    d_status = None if status is None else _ints(status, where, "status", index, (1,))
+    handle, context = _place(where, index, stream)
+    _launch(_lk._lib.loopkv_paged_append, context, ctypes.addressof(pool), cells.tobytes(), cells.size, rows,
+            d_slots, ctypes.addressof(kr), ctypes.addressof(vr), d_status, handle)
+
+
+@functools.lru_cache(maxsize=256)
+def _work_bytes(batch, width, group, cells, pages, page_size, heads, dim, fmt):
+    """Workspace of a decode, which its sizes alone decide."""
+    some = 16  # an aligned address that nothing reads
+    rc, nbytes = _lk.loopkv_paged_workspace(
+        _lk.loopkv_page_pool(cells, pages, page_size, heads, dim, fmt, some, some,
+                             some if fmt == _lk.LOOPKV_PAGE_Q8 else None),
+        _lk.loopkv_paged_desc(batch, width, group, 0.0))
+    _check(rc, "loopkv_paged_workspace")
+    return nbytes
 
 
 def paged_decode(cells, q, k_pages, v_pages, table, lengths, meta=None, cur_k=None, cur_v=None,
@@ -243,55 +246,57 @@ def paged_decode(cells, q, k_pages, v_pages, table, lengths, meta=None, cur_k=No
     true.  Returns out in q's dtype and shape; ``lse`` (fp32 [listed cells,
     batch, query heads]) receives the natural-log sum of exponentials.  A
     request without tokens gives zeros and -infinity."""
-    import torch
     where = "paged_decode"
-    pool, dtype = _pool(k_pages, v_pages, meta, where)
-    dev = k_pages.device
+    pool, dtype, index = _pool(k_pages, v_pages, meta, where)
     cells = _cells(cells, where)
     batch, width = _shape(table, where, "table", 2)
-    heads, dim = pool.n_kv_heads, pool.head_dim
-    qr = _rows(q, where, "q", dtype, dev, (cells.size, batch, None, dim))
+    n_cells, heads, dim = cells.size, pool.n_kv_heads, pool.head_dim
+    qr = _rows(q, where, "q", dtype, index, (n_cells, batch, None, dim))
     q_heads = q.shape[2]
-    if q_heads % heads or not 1 <= q_heads // heads <= _lk.LOOPKV_MAX_PAGED_GROUP:
+    if heads < 1 or q_heads % heads or not 1 <= q_heads // heads <= _lk.LOOPKV_MAX_PAGED_GROUP:
         raise _invalid(where, "%d query heads on %d KV heads: 1 to %d each" % (
             q_heads, heads, _lk.LOOPKV_MAX_PAGED_GROUP))
-    d_table = _ints(table, where, "table", dev, (batch, width))
-    d_len = _ints(lengths, where, "lengths", dev, (batch,))
+    d_table = _ints(table, where, "table", index, (batch, width))
+    d_len = _ints(lengths, where, "lengths", index, (batch,))
     kr = vr = flags = None
     if (cur_k is None) != (cur_v is None):
         raise _invalid(where, "cur_k and cur_v come together")
     if current is not None:
         flags = np.ascontiguousarray(current, dtype=np.uint8).reshape(-1)
-        if flags.size != cells.size:
-            raise _invalid(where, "current must hold %d values, not %d" % (cells.size, flags.size))
+        if flags.size != n_cells:
+            raise _invalid(where, "current must hold %d values, not %d" % (n_cells, flags.size))
         if cur_k is None and flags.any():
             raise _invalid(where, "cur_k and cur_v are required where current is true")
+        flags = flags.tobytes()
     if cur_k is not None:
-        kr = _rows(cur_k, where, "cur_k", dtype, dev, (cells.size, batch, heads, dim))
-        vr = _rows(cur_v, where, "cur_v", dtype, dev, (cells.size, batch, heads, dim))
+        kr = _rows(cur_k, where, "cur_k", dtype, index, (n_cells, batch, heads, dim))
+        vr = _rows(cur_v, where, "cur_v", dtype, index, (n_cells, batch, heads, dim))
         if flags is None:
-            flags = np.ones(cells.size, np.uint8)
-    desc = _lk.loopkv_paged_desc(batch, width, q_heads // heads, float(sm_scale))
-    d_status = _status(status, where, dev)
-    rc, nbytes = _lk.loopkv_paged_workspace(pool, desc)
-    _check(rc, "loopkv_paged_workspace")
-    context, handle = _place(where, dev, stream)
-    with context:  # memory made here belongs to the stream of the launch
-        if out is None:
-            out = torch.empty(tuple(q.shape), dtype=dtype, device=dev)
-        else:
-            _lk._need(out, where, "out", (dtype,), shape=q.shape, device=dev)
-        if lse is not None:
-            _lk._need(lse, where, "lse", (torch.float32,), shape=q.shape[:-1], device=dev)
-        work = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            flags = b"\1" * n_cells
+    group = q_heads // heads
+    desc = _lk.loopkv_paged_desc(batch, width, group, float(sm_scale))
+    d_status = None if status is None else _ints(status, where, "status", index, (1,))
+    d_out = None if out is None else _full(out, where, "out", dtype, index, q.shape)
+    d_lse = None if lse is None else _full(lse, where, "lse", _F32, index, q.shape[:3])
+    nbytes = _work_bytes(batch, width, group, pool.n_cells, pool.n_pages, pool.page_size, heads, dim, pool.format)
+    handle, context = _place(where, index, stream)
+
+    def launch():  # memory made here belongs to the stream of the launch
+        work = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        got = torch.empty(q.shape, dtype=dtype, device=q.device) if out is None else out
         rc = _lk._lib.loopkv_paged_decode(
-            ctypes.addressof(pool), ctypes.addressof(desc), cells.ctypes.data,
-            None if flags is None else flags.ctypes.data, cells.size, d_table, d_len,
+            ctypes.addressof(pool), ctypes.addressof(desc), cells.tobytes(), flags, n_cells, d_table, d_len,
             ctypes.addressof(qr), None if kr is None else ctypes.addressof(kr),
-            None if vr is None else ctypes.addressof(vr), out.data_ptr(),
-            None if lse is None else lse.data_ptr(), work.data_ptr(), nbytes, d_status, handle)
-    _check(rc, "loopkv_paged_decode")
-    return out
+            None if vr is None else ctypes.addressof(vr), got.data_ptr() if d_out is None else d_out, d_lse,
+            work.data_ptr(), nbytes, d_status, handle)
+        if rc:
+            _check(rc, "loopkv_paged_decode")
+        return got
+
+    if context is None:
+        return launch()
+    with context:
+        return launch()
 
 
 class PagedCache:
@@ -303,10 +308,9 @@ class PagedCache:
 
     def __init__(self, n_loops, n_layers, n_kv_heads, head_dim, n_pages, page_size, max_batch,
                  max_pages, shared=(), dtype=None, sm_scale=0.0, device="cuda"):
-        import torch
         where = "PagedCache"
         dtype = torch.bfloat16 if dtype is None else dtype
-        if dtype not in _formats():
+        if dtype not in _FORMATS:
             raise _invalid(where, "pages of %s" % dtype)
         if n_loops < 1 or n_layers < 1:
             raise _invalid(where, "%d loops of %d layers" % (n_loops, n_layers))
@@ -383,7 +387,6 @@ class PagedCache:
         """Wait for ``stream``, read and clear the status word; raises
         LoopKVError (LOOPKV_ERR_CAPACITY if requests were refused for want of
         room, else LOOPKV_ERR_DEVICE) when it is not 0."""
-        import torch
         with torch.cuda.stream(stream):
             bits = int(self.status.item())
             if bits:
