@@ -67,9 +67,12 @@ constexpr int kSms = 148;
 constexpr int kMaxWorkers = kSms * 4;
 constexpr int kTile = 16;            // tokens of a warp's step
 constexpr int kMinCost = 2 * kWarps;  // cost a worker takes at least
-constexpr int kUnitCost = 16;          // tiles that a unit's start and end are worth
+constexpr int kUnitCost = 24;         // tiles that a unit's start and end are worth
+constexpr int kEmptyCost = 2;         // and a unit without tokens, which is only written
 constexpr int kMaxRows = LOOPKV_MAX_PAGED_GROUP;  // query rows of a set
 constexpr int kJoinThreads = 512;
+constexpr int kJoinBlocks = 2 * kSms;
+constexpr int kFewParts = 16;         // a warp joins fewer continuations than this
 constexpr int kCurrentBit = 1 << 30;  // in a set's cell: the last token is in cur_k / cur_v
 
 struct RowView {
@@ -169,6 +172,10 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+__device__ __forceinline__ float lse_of(float top, float sum) {
+  return sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+}
+
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) {
   return __byte_perm(a, b, s);
 }
@@ -252,8 +259,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
   const int64_t page_rows = (int64_t)p.heads * p.div.size;
   uint32_t status = 0;
 
-  // Cost of a unit of every request: its tiles (at least one: a unit without
-  // tokens is written too) and its start and end.
+  // Cost of a unit of every request: its tiles and its start and end.
   {
     const int per = (p.batch + kThreads - 1) / kThreads;
     int sum = 0;
@@ -265,7 +271,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
         status |= LOOPKV_PAGE_BAD_LENGTH;
         n = 0;
       }
-      const int t = kUnitCost + max(1, (n + kTile - 1) / kTile);
+      const int t = n == 0 ? kEmptyCost : kUnitCost + (n + kTile - 1) / kTile;
       prefix[b + 1] = t;
       sum += t;
     }
@@ -308,23 +314,18 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
   }
 
   while (x < x1) {
-    // position i of a unit's cost is its tile i - kUnitCost
-    const int cost = prefix[b + 1] - prefix[b], tiles = cost - kUnitCost;
+    const int cost = prefix[b + 1] - prefix[b];
     const int64_t rem = x - (int64_t)prefix[b] * per_request;
     const int u = (int)(rem / cost), from = (int)(rem - (int64_t)u * cost);
     const int set = u / p.heads, h = u - set * p.heads;
     const int upto = (int)min((int64_t)cost, from + (x1 - x));
-    const int t0 = max(0, from - kUnitCost), t1 = upto - kUnitCost;
-    x += upto - from;
-    if (t1 <= 0) break;  // the share ends before the unit's first tile
     const int first = sets.first[set], rows = (sets.first[set + 1] - first) * p.group;
     int n = p.len[b];
     if (n < 0 || n > p.max_pages * p.div.size) n = 0;
-    const bool current = (sets.cell[set] & kCurrentBit) != 0 && n > 0;
-    const int64_t cell_row = (int64_t)(sets.cell[set] & ~kCurrentBit) * p.cell_rows + (int64_t)h * p.div.size;
-    const int np = current ? n - 1 : n;  // tokens read from pages
+    x += upto - from;
     if (n == 0) {
-      for (int i = tid; i < rows * (D / 8); i += kThreads) {
+      // written by the worker whose share has its first position
+      for (int i = from == 0 ? tid : rows * (D / 8); i < rows * (D / 8); i += kThreads) {
         const int row = i / (D / 8), mem = row / p.group, li = sets.member[first + mem];
         const int64_t at = (((int64_t)li * p.batch + b) * p.heads + h) * p.group + row - mem * p.group;
         reinterpret_cast<uint4*>(p.out + at * D)[i - row * (D / 8)] = make_uint4(0, 0, 0, 0);
@@ -333,6 +334,12 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
       if (x == (int64_t)prefix[b + 1] * per_request) ++b;
       continue;
     }
+    // position i of a unit's cost is its tile i - kUnitCost
+    const int tiles = cost - kUnitCost, t0 = max(0, from - kUnitCost), t1 = upto - kUnitCost;
+    if (t1 <= 0) break;  // the share ends before the unit's first tile
+    const bool current = (sets.cell[set] & kCurrentBit) != 0 && n > 0;
+    const int64_t cell_row = (int64_t)(sets.cell[set] & ~kCurrentBit) * p.cell_rows + (int64_t)h * p.div.size;
+    const int np = current ? n - 1 : n;  // tokens read from pages
 
     // The page of token (lane & 15) of a tile (FLAT: of its first token), loaded
     // a step before the tile is copied.  A tile is then a row (FLAT: the first
@@ -684,7 +691,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
         const int64_t to = (((int64_t)li * p.batch + b) * p.heads + h) * p.group + i - mem * p.group;
         const float y = sum == 0.f ? 0.f : acc / sum;
         p.out[to * D + d] = (uint16_t)(M::pack(y, y) & 0xffffu);
-        if (d == 0 && p.lse) p.lse[to] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+        if (d == 0 && p.lse) p.lse[to] = lse_of(top, sum);
       } else {
         part[idx] = acc;
         if (d == 0) p.stat[slot * p.rows + i] = make_float2(top, sum);
@@ -702,83 +709,162 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
   if (status && p.status) atomicOr(p.status, status);
 }
 
-// Join the parts of a unit that worker blockIdx.x began and did not end:
-// its own (slot 2 i + 1) and those of the workers behind it (slots 2 (i + k)).
-// A block does one query row: all parts' maxima and sums at once, then their
-// channels, four to a thread, the parts dealt to groups of D / 4 threads, and
-// the groups' sums.  Launched while the decode still runs (every block waits
-// for its end before it reads).  What bounds it: four dependent round trips to
-// L2; with one thread a channel and a running maximum over the parts, two
-// units of 300 parts took 17 us.
+// Where a row of a unit goes.
+__device__ __forceinline__ int64_t out_row(const PagedDecodeParams& p, const Sets& sets, int unit, int row) {
+  const int h = unit % p.heads, sb = unit / p.heads, set = sb / p.batch, b = sb - set * p.batch;
+  const int first = sets.first[set], mem = row / p.group;
+  if (first + mem >= sets.first[set + 1]) return -1;  // a smaller set
+  return (((int64_t)sets.member[first + mem] * p.batch + b) * p.heads + h) * p.group + row - mem * p.group;
+}
+
+// Join the parts of the units that a worker i began and did not end: its own
+// (slot 2 i + 1) and those of the workers behind it (slots 2 (i + k)).  An item
+// is one query row of such a unit.  Up to kFewParts parts are a warp's work;
+// more are a block's: all parts' maxima and sums at once, then their channels,
+// four to a thread, the parts dealt to groups of D / 4 threads, and the groups'
+// sums.  Launched while the decode still runs (every block waits for its end
+// before it reads).  What bounds it: four dependent round trips to L2.  With
+// one thread a channel and a running maximum over the parts, 2 units of 300
+// parts took 17 us; with a block per worker and row, 2000 rows of 2 parts 8 us.
 template <int D, int FMT>
 __global__ void __launch_bounds__(kJoinThreads)
 paged_join_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_constant__ Sets sets) {
   using M = Mma<FMT>;
-  constexpr int WARPS = kJoinThreads / 32, GROUPS = kJoinThreads / (D / 4);
-  __shared__ float factor[kMaxWorkers], wm[WARPS], wl[WARPS];
-  __shared__ float4 sa[GROUPS][D / 4];
-  const int i = blockIdx.x, row = blockIdx.y, tid = threadIdx.x;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int more = p.split[2 * i + 1];
-  if (more == 0) return;
-  const int unit = p.split[2 * i];
-  const int h = unit % p.heads, sb = unit / p.heads, set = sb / p.batch, b = sb - set * p.batch;
-  const int first = sets.first[set], rows = (sets.first[set + 1] - first) * p.group;
-  if (row >= rows) return;
-  auto slot = [&](int k) { return k == 0 ? 2 * i + 1 : 2 * (i + k); };
+  constexpr int WARPS = kJoinThreads / 32, LANES = D / 4, GROUPS = kJoinThreads / LANES;
   constexpr int PER = (kMaxWorkers + kJoinThreads - 1) / kJoinThreads;
-  float2 mine[PER];
-  float top = -INFINITY, sum = 0.f;
+  __shared__ int2 split[kMaxWorkers];
+  __shared__ uint16_t list[kMaxWorkers];
+  __shared__ int counts[PER * WARPS];
+  __shared__ float factor[kMaxWorkers], wm[WARPS], wl[WARPS];
+  __shared__ float4 sa[GROUPS][LANES];
+  const int tid = threadIdx.x, lane = tid & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the units of many parts, in order
+  bool many[PER];
+  uint32_t ballot[PER];
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
-    const int k = tid + j * kJoinThreads;
-    mine[j] = k <= more ? p.stat[slot(k) * p.rows + row] : make_float2(-INFINITY, 0.f);
-    top = fmaxf(top, mine[j].x);
+    const int i = tid + j * kJoinThreads;
+    const int2 mine = i < p.workers ? reinterpret_cast<const int2*>(p.split)[i] : make_int2(0, 0);
+    if (i < p.workers) split[i] = mine;
+    many[j] = mine.y >= kFewParts;
+    ballot[j] = __ballot_sync(0xffffffffu, many[j]);
+    if (lane == 0) counts[j * WARPS + (tid >> 5)] = __popc(ballot[j]);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if ((tid & 31) == 0) wm[tid >> 5] = top;
   __syncthreads();
+  static_assert(PER * WARPS == 32, "a count a lane");
+  const int count = counts[lane];
+  int upto = count;
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) top = fmaxf(top, wm[w]);
-  const float base = top == -INFINITY ? 0.f : top;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  const int n_list = __shfl_sync(0xffffffffu, upto, 31);
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
-    const int k = tid + j * kJoinThreads;
-    const float f = exp2_fast(mine[j].x - base);
-    if (k <= more) factor[k] = f;
-    sum = fmaf(f, mine[j].y, sum);
+    const int before = __shfl_sync(0xffffffffu, upto - count, j * WARPS + (tid >> 5));
+    if (many[j]) list[before + __popc(ballot[j] & ((1u << lane) - 1u))] = (uint16_t)(tid + j * kJoinThreads);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if ((tid & 31) == 0) wl[tid >> 5] = sum;
   __syncthreads();
-  const int lane4 = tid % (D / 4), group = tid / (D / 4);
-  float4 acc4 = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto slot = [&](int i, int k) { return k == 0 ? 2 * i + 1 : 2 * (i + k); };
+
+  for (int it = blockIdx.x * WARPS + (tid >> 5); it < p.workers * p.rows; it += gridDim.x * WARPS) {
+    const int i = it / p.rows, row = it - i * p.rows, more = split[i].y;
+    if (more == 0 || more >= kFewParts) continue;
+    const int64_t to = out_row(p, sets, split[i].x, row);
+    if (to < 0) continue;
+    const float2 mine = lane <= more ? p.stat[slot(i, lane) * p.rows + row] : make_float2(-INFINITY, 0.f);
+    float top = mine.x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float f = exp2_fast(mine.x - (top == -INFINITY ? 0.f : top));
+    float sum = f * mine.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-  for (int k = group; k <= more; k += GROUPS) {
-    const float4 a = reinterpret_cast<const float4*>(p.part + ((int64_t)slot(k) * p.rows + row) * D)[lane4];
-    const float f = factor[k];
-    acc4.x = fmaf(f, a.x, acc4.x);
-    acc4.y = fmaf(f, a.y, acc4.y);
-    acc4.z = fmaf(f, a.z, acc4.z);
-    acc4.w = fmaf(f, a.w, acc4.w);
+    for (int k0 = 0; k0 <= more; k0 += 32 / LANES) {
+      const int k = k0 + lane / LANES;
+      const float g = __shfl_sync(0xffffffffu, f, k);
+      if (k > more) continue;
+      const float4 a = reinterpret_cast<const float4*>(p.part + ((int64_t)slot(i, k) * p.rows + row) * D)[lane % LANES];
+      acc.x = fmaf(g, a.x, acc.x);
+      acc.y = fmaf(g, a.y, acc.y);
+      acc.z = fmaf(g, a.z, acc.z);
+      acc.w = fmaf(g, a.w, acc.w);
+    }
+#pragma unroll
+    for (int o = 16; o >= LANES; o >>= 1) {
+      acc.x += __shfl_xor_sync(0xffffffffu, acc.x, o);
+      acc.y += __shfl_xor_sync(0xffffffffu, acc.y, o);
+      acc.z += __shfl_xor_sync(0xffffffffu, acc.z, o);
+      acc.w += __shfl_xor_sync(0xffffffffu, acc.w, o);
+    }
+    const bool none = sum == 0.f;
+    if (lane < LANES)
+      reinterpret_cast<uint2*>(p.out + to * D)[lane] =
+          make_uint2(M::pack(none ? 0.f : acc.x / sum, none ? 0.f : acc.y / sum),
+                     M::pack(none ? 0.f : acc.z / sum, none ? 0.f : acc.w / sum));
+    if (lane == 0 && p.lse) p.lse[to] = lse_of(top, sum);
   }
-  sa[group][lane4] = acc4;
-  __syncthreads();
-  if (tid >= D) return;
-  const int d = tid;
-  float acc = 0.f;
-  sum = 0.f;
+
+  for (int it = blockIdx.x; it < n_list * p.rows; it += gridDim.x) {
+    const int at = it / p.rows, row = it - at * p.rows, i = list[at], more = split[i].y;
+    const int64_t to = out_row(p, sets, split[i].x, row);
+    if (to < 0) continue;
+    float2 mine[PER];
+    float top = -INFINITY, sum = 0.f;
 #pragma unroll
-  for (int g = 0; g < GROUPS; ++g) acc += reinterpret_cast<const float*>(sa[g])[d];
+    for (int j = 0; j < PER; ++j) {
+      const int k = tid + j * kJoinThreads;
+      mine[j] = k <= more ? p.stat[slot(i, k) * p.rows + row] : make_float2(-INFINITY, 0.f);
+      top = fmaxf(top, mine[j].x);
+    }
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) sum += wl[w];
-  const int mem = row / p.group, li = sets.member[first + mem];
-  const int64_t to = (((int64_t)li * p.batch + b) * p.heads + h) * p.group + row - mem * p.group;
-  const float y = sum == 0.f ? 0.f : acc / sum;
-  p.out[to * D + d] = (uint16_t)(M::pack(y, y) & 0xffffu);
-  if (d == 0 && p.lse) p.lse[to] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) wm[tid >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) top = fmaxf(top, wm[w]);
+    const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const int k = tid + j * kJoinThreads;
+      const float f = exp2_fast(mine[j].x - base);
+      if (k <= more) factor[k] = f;
+      sum = fmaf(f, mine[j].y, sum);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) wl[tid >> 5] = sum;
+    __syncthreads();
+    const int lane4 = tid % LANES, group = tid / LANES;
+    float4 acc4 = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int k = group; k <= more; k += GROUPS) {
+      const float4 a = reinterpret_cast<const float4*>(p.part + ((int64_t)slot(i, k) * p.rows + row) * D)[lane4];
+      const float f = factor[k];
+      acc4.x = fmaf(f, a.x, acc4.x);
+      acc4.y = fmaf(f, a.y, acc4.y);
+      acc4.z = fmaf(f, a.z, acc4.z);
+      acc4.w = fmaf(f, a.w, acc4.w);
+    }
+    sa[group][lane4] = acc4;
+    __syncthreads();
+    if (tid < D) {
+      float acc = 0.f;
+      sum = 0.f;
+#pragma unroll
+      for (int g = 0; g < GROUPS; ++g) acc += reinterpret_cast<const float*>(sa[g])[tid];
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) sum += wl[w];
+      const float y = sum == 0.f ? 0.f : acc / sum;
+      p.out[to * D + tid] = (uint16_t)(M::pack(y, y) & 0xffffu);
+      if (tid == 0 && p.lse) p.lse[to] = lse_of(top, sum);
+    }
+    __syncthreads();  // shared memory is free for the next item
+  }
 }
 
 size_t work_bytes_of(int D) {
@@ -797,7 +883,7 @@ loopkv_status launch_decode_kernel(PagedDecodeParams p, const Sets& sets, cudaSt
   kernel<<<p.workers, kThreads, smem, stream>>>(p, sets);
   if (cudaGetLastError() != cudaSuccess) return LOOPKV_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)p.workers, (unsigned)p.rows, 1);
+  cfg.gridDim = dim3(kJoinBlocks, 1, 1);
   cfg.blockDim = dim3(kJoinThreads, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
