@@ -26,6 +26,7 @@ import functools
 import numpy as np
 import torch
 
+from . import _paged
 from . import loopkv as _lk
 from .loopkv import _check, _invalid
 
@@ -35,9 +36,15 @@ _FORMATS = {torch.bfloat16: (_lk.LOOPKV_PAGE_BF16, torch.bfloat16),
             torch.uint8: (_lk.LOOPKV_PAGE_Q8, torch.bfloat16)}
 _I32, _F32 = torch.int32, torch.float32
 
-# A decode step's calls are a few microseconds of device time each, so checks
-# are written for the case that they pass, with few attribute reads, and what
-# is wrong is found out afterwards.
+# A decode step's calls are a few microseconds of device time each, so a call in
+# its plain form (the current device and its current stream, nothing wrong with
+# the arguments) is checked and launched by _paged (csrc/paged_binding.cpp).  It
+# returns _NOT_PLAIN, having done nothing, for the rest, which goes the way
+# written here: a stream that is given, another device, what to tell the caller.
+_NOT_PLAIN = -1
+_paged.bind(*(ctypes.cast(getattr(_lk._lib, name), ctypes.c_void_p).value for name in (
+    "loopkv_page_map", "loopkv_page_release", "loopkv_paged_append", "loopkv_paged_workspace",
+    "loopkv_paged_decode")))
 
 
 def _place(where, index, stream):
@@ -117,6 +124,13 @@ def page_map(lengths, n_new, table, free, free_count, page_size, slots, starts, 
     not fit (pages, table width, rows) is refused whole: its length stays and
     ``status`` gets a bit.  Returns (slots, starts)."""
     where = "page_map"
+    if stream is None:
+        rc = _paged.page_map(lengths, n_new, table, free, free_count, page_size, slots, starts, newest,
+                             lengths_out, free_count_out, status)
+        if rc != _NOT_PLAIN:
+            if rc:
+                _check(rc, "loopkv_page_map")
+            return slots, starts
     batch, width = _shape(table, where, "table", 2)
     (n_pages,), (rows,) = _shape(free, where, "free", 1), _shape(slots, where, "slots", 1)
     page_size = _size(page_size, where, "page_size")
@@ -146,6 +160,13 @@ def page_release(lengths, new_lengths, table, free, free_count, page_size, lengt
     ``lengths_out`` / ``free_count_out`` (None: in place); the table stays as
     it is.  A request whose new length is not in 0 .. its length keeps it."""
     where = "page_release"
+    if stream is None:
+        rc = _paged.page_release(lengths, new_lengths, table, free, free_count, page_size, lengths_out,
+                                 free_count_out, status)
+        if rc != _NOT_PLAIN:
+            if rc:
+                _check(rc, "loopkv_page_release")
+            return
     batch, width = _shape(table, where, "table", 2)
     (n_pages,) = _shape(free, where, "free", 1)
     page_size = _size(page_size, where, "page_size")
@@ -209,6 +230,12 @@ def paged_append(cells, k, v, slots, k_pages, v_pages, meta=None, status=None, s
     is stored of that input).  Rows with slot -1 are skipped.  uint8 pages get
     codes and ``meta`` their scales and zero points."""
     where = "paged_append"
+    if stream is None:
+        rc = _paged.paged_append(cells, k, v, slots, k_pages, v_pages, meta, status)
+        if rc != _NOT_PLAIN:
+            if rc:
+                _check(rc, "loopkv_paged_append")
+            return
     pool, dtype, index = _pool(k_pages, v_pages, meta, where)
     cells = _cells(cells, where)
     (rows,) = _shape(slots, where, "slots", 1)
@@ -247,6 +274,13 @@ def paged_decode(cells, q, k_pages, v_pages, table, lengths, meta=None, cur_k=No
     batch, query heads]) receives the natural-log sum of exponentials.  A
     request without tokens gives zeros and -infinity."""
     where = "paged_decode"
+    if stream is None:
+        got = _paged.paged_decode(cells, q, k_pages, v_pages, table, lengths, meta, cur_k, cur_v, current, out,
+                                  lse, sm_scale, status)
+        if type(got) is not int:
+            return got
+        if got != _NOT_PLAIN:
+            _check(got, "loopkv_paged_decode")
     pool, dtype, index = _pool(k_pages, v_pages, meta, where)
     cells = _cells(cells, where)
     batch, width = _shape(table, where, "table", 2)

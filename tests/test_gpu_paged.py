@@ -546,6 +546,42 @@ def test_decode_on_another_stream(dev):
     assert (got[0] == want[0]).all() and (got[1] == want[1]).all()
 
 
+def test_every_way_of_calling_gives_the_same(dev):
+    # the short way (current stream) and the long one (a stream given, a tensor subclass, cells as
+    # a tuple or range), lists and arrays of cells, outputs given or made
+    import torch
+    from loop_aware_quantized_b200 import paged_append, paged_decode
+
+    class Other(torch.Tensor):
+        pass
+
+    c = Case(dev, "q8", [40, 0, 130], heads=2, group=2, dim=64, cells=(1, 0, 1), seed=20)
+    t, n = ints(c.table, dev), ints(c.lengths, dev)
+    args = (c.kp, c.vp, t, n)
+    kw = dict(meta=c.meta, cur_k=c.cur[0], cur_v=c.cur[1])
+    flags = [True, False, True]
+    want = paged_decode([1, 0, 1], c.q, *args, **kw, current=np.array(flags))
+    calls = [dict(cells=x, **kw, current=f) for x, f in (
+        ((1, 0, 1), flags), (np.array([1, 0, 1]), np.array(flags)), (np.array([1, 0, 1], np.int32), flags),
+        (np.array([1, 0, 1], np.int16), np.array(flags, np.uint8)), ([np.int64(1), 0, 1], tuple(flags)),
+        (np.array([1, 5, 0, 5, 1])[::2], np.array(flags)))]
+    calls += [dict(cells=[1, 0, 1], **kw, current=flags, stream=torch.cuda.current_stream()),
+              dict(cells=[1, 0, 1], **{**kw, "cur_k": c.cur[0].as_subclass(Other)}, current=flags)]
+    for call in calls:
+        out = torch.full_like(c.q, 5)
+        assert paged_decode(q=c.q, k_pages=c.kp, v_pages=c.vp, table=t, lengths=n, out=out, **call) is out
+        assert (out == want).all()
+        assert (paged_decode(q=c.q, k_pages=c.kp, v_pages=c.vp, table=t, lengths=n, **call) == want).all()
+    slots = ints([3, -1, 40], dev)
+    pools = []
+    for cells, stream in (([1, -1, 0], None), ((1, -1, 0), None), (np.array([1, -1, 0]), torch.cuda.current_stream())):
+        pool = [x.clone() for x in (c.kp, c.vp, c.meta)]
+        paged_append(cells, c.cur[0], c.cur[1], slots, pool[0], pool[1], meta=pool[2], stream=stream)
+        pools.append([as_bytes(x) for x in pool])
+    assert all(np.array_equal(x, y) for p in pools[1:] for x, y in zip(p, pools[0]))
+    assert not np.array_equal(pools[0][0], as_bytes(c.kp))
+
+
 def test_calls_at_once_on_two_streams(dev):
     # each call has a workspace of its own
     import torch

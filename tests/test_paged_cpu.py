@@ -175,6 +175,21 @@ def test_binding_refuses_before_the_library(lk):
                                  page_size=16, max_batch=2, max_pages=4, device="cpu"), **kw})
 
 
+def test_short_way_declines_what_it_does_not_handle(lk):
+    # nothing but kNotPlain for arguments of any kind, and no error left behind
+    import torch
+    from loop_aware_quantized_b200 import _paged
+    host = torch.zeros((2, 2), dtype=torch.int32)
+    odd = [None, 0, -1, 1 << 70, 2.5, "x", b"x", [], [1 << 40], [True], (1, 2), np.zeros(3), np.zeros((2, 2), np.int32),
+           np.arange(300), host, host[0], torch.zeros(3), torch.nn.Parameter(torch.zeros(2)), object()]
+    for name, n in (("page_map", 12), ("page_release", 9), ("paged_append", 8), ("paged_decode", 14)):
+        fn = getattr(_paged, name)
+        assert fn() == -1 and fn(*[None] * (n + 1)) == -1
+        for i in range(len(odd)):
+            assert fn(*[odd[(i + j * 7) % len(odd)] for j in range(n)]) == -1
+            assert fn(*[odd[i]] * n) == -1
+
+
 def test_cache_maps_shared_cells_to_the_final_loop(lk):
     from loop_aware_quantized_b200 import PagedCache
     c = PagedCache(3, 2, 1, 64, 4, 16, 2, 4, shared=[0, 3], device="cpu")
