@@ -98,8 +98,10 @@ struct PagedDecodeParams {
   uint32_t* status;
   int32_t n_sets, batch, heads, group, max_pages, n_pages, workers;
   int32_t rows;       // query rows of the largest set
-  int64_t cell_rows;  // token rows of a pool cell
+  uint32_t cell_rows; // token rows of a pool cell
   float scale2;       // sm_scale * log2(e)
+  float unit2;        // the same for a score as the products give it (Q8: times 2^69)
+  float slack;        // kSlack in those units
   PageDiv div;
 };
 
@@ -188,6 +190,9 @@ __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, bool on
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0)
                : "memory");
 }
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copy_wait() {
@@ -243,6 +248,8 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
   float* const sz = sl + (kWarps + 1) * kMaxRows;                // [kWarps][kMaxRows] zero-point sums (Q8)
   int* const prefix = reinterpret_cast<int*>(sz + kWarps * kMaxRows);  // [batch + 1] tiles before a request
   __shared__ int warp_sums[kWarps];
+  __shared__ int64_t out_at[kMaxRows];
+  __shared__ const uint16_t* cur_at[kMaxRows];
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
@@ -256,7 +263,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
   // (rows begin on multiples of their size, so a later piece is an exclusive or away)
   const uint32_t k_at = k_row * S::kRowBytes + ((k_piece ^ S::swizzle(k_row)) << 4);
   const uint32_t v_at = v_row * S::kRowBytes + ((v_piece ^ S::swizzle(v_row)) << 4);
-  const int64_t page_rows = (int64_t)p.heads * p.div.size;
+  const uint32_t page_rows = (uint32_t)p.heads * (uint32_t)p.div.size;  // (a pool's rows are numbered in 32 bits)
   uint32_t status = 0;
 
   // Cost of a unit of every request: its tiles and its start and end.
@@ -338,42 +345,51 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
     const int tiles = cost - kUnitCost, t0 = max(0, from - kUnitCost), t1 = upto - kUnitCost;
     if (t1 <= 0) break;  // the share ends before the unit's first tile
     const bool current = (sets.cell[set] & kCurrentBit) != 0 && n > 0;
-    const int64_t cell_row = (int64_t)(sets.cell[set] & ~kCurrentBit) * p.cell_rows + (int64_t)h * p.div.size;
+    const uint32_t cell_row = (uint32_t)(sets.cell[set] & ~kCurrentBit) * p.cell_rows + (uint32_t)(h * p.div.size);
     const int np = current ? n - 1 : n;  // tokens read from pages
 
     // The page of token (lane & 15) of a tile (FLAT: of its first token), loaded
     // a step before the tile is copied.  A tile is then a row (FLAT: the first
     // one; else the lane's token's) and a bit per token to be read.
     const int32_t* const entry = p.table + (int64_t)b * p.max_pages;
-    auto page_of = [&](int tile) -> int {
-      const int pos = tile * kTile + (FLAT ? 0 : lane & 15);
-      return tile < t1 && pos < np ? __ldg(entry + p.div.page(pos)) : INT_MIN;
+    struct Next {
+      int page, off;
     };
-    auto rows_of = [&](int tile, int page, uint32_t* row) -> uint32_t {
+    auto page_of = [&](int tile) -> Next {
       const int pos = tile * kTile + (FLAT ? 0 : lane & 15);
-      const bool good = page >= 0 && page < p.n_pages;
-      if (!good && page != INT_MIN) status |= LOOPKV_PAGE_BAD_PAGE;
-      *row = good ? (uint32_t)(cell_row + (int64_t)page * page_rows + (pos - p.div.page(pos) * p.div.size)) : 0u;
-      if (FLAT) return good ? (1u << min(kTile, np - pos)) - 1u : 0u;
+      if (tile >= t1 || pos >= np) return {INT_MIN, 0};
+      const int j = p.div.page(pos);
+      return {__ldg(entry + j), pos - j * p.div.size};
+    };
+    auto rows_of = [&](int tile, Next at, uint32_t* row) -> uint32_t {
+      const bool good = at.page >= 0 && at.page < p.n_pages;
+      if (!good && at.page != INT_MIN) status |= LOOPKV_PAGE_BAD_PAGE;
+      *row = good ? cell_row + (uint32_t)at.page * page_rows + (uint32_t)at.off : 0u;
+      if (FLAT) return good ? (1u << min(kTile, np - tile * kTile)) - 1u : 0u;
       return __ballot_sync(0xffffffffu, good) & 0xffffu;
     };
     auto copy_rows = [&](uint32_t at, const uint8_t* src, uint32_t row, uint32_t bits) {
       at += copy_row * S::kRowBytes;
       src += 16 * piece;
-      bits >>= copy_row;
+      auto dst = [&](int t) { return at + t * S::kRowBytes + ((piece ^ S::swizzle(t + copy_row)) << 4); };
       if constexpr (FLAT) {
         src += ((uint64_t)row + copy_row) * S::kRowBytes;
+        if (bits == 0xffffu) {
 #pragma unroll
-        for (int i = 0; i < S::kCopies; ++i) {
-          const int t = i * S::kRowsPerCopy;
-          copy16(at + t * S::kRowBytes + ((piece ^ S::swizzle(t + copy_row)) << 4), src + t * S::kRowBytes, (bits >> t & 1) != 0);
+          for (int i = 0; i < S::kCopies; ++i)
+            copy16(dst(i * S::kRowsPerCopy), src + i * S::kRowsPerCopy * S::kRowBytes);
+        } else {
+          bits >>= copy_row;
+#pragma unroll
+          for (int i = 0; i < S::kCopies; ++i)
+            copy16(dst(i * S::kRowsPerCopy), src + i * S::kRowsPerCopy * S::kRowBytes, (bits >> (i * S::kRowsPerCopy) & 1) != 0);
         }
       } else {
+        bits >>= copy_row;
 #pragma unroll
         for (int i = 0; i < S::kCopies; ++i) {
-          const int t = i * S::kRowsPerCopy;
-          const uint32_t from = __shfl_sync(0xffffffffu, row, t + copy_row);
-          copy16(at + t * S::kRowBytes + ((piece ^ S::swizzle(t + copy_row)) << 4), src + (uint64_t)from * S::kRowBytes, (bits >> t & 1) != 0);
+          const uint32_t from = __shfl_sync(0xffffffffu, row, i * S::kRowsPerCopy + copy_row);
+          copy16(dst(i * S::kRowsPerCopy), src + (uint64_t)from * S::kRowBytes, (bits >> (i * S::kRowsPerCopy) & 1) != 0);
         }
       }
     };
@@ -391,12 +407,12 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
 
     // The first tiles' copies; valid holds 16 bits a stage, this step's lowest.
     uint64_t valid = 0;
-    int next_page;
+    Next next;
     {
-      int pages[S::kStages];
+      Next pages[S::kStages];
 #pragma unroll
       for (int s = 0; s < S::kStages; ++s) pages[s] = page_of(t0 + warp + s * kWarps);
-      next_page = page_of(t0 + warp + S::kStages * kWarps);
+      next = page_of(t0 + warp + S::kStages * kWarps);
 #pragma unroll
       for (int s = 0; s < S::kStages; ++s) {
         uint32_t row;
@@ -448,15 +464,16 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
       }
-      qsum[half] = sum * p.scale2;
+      qsum[half] = sum * 0x1p-69f;
     }
 
     float o[NT][S::kMTiles][4];
-    float m[NT], l[NT], z[NT];
+    // running maximum in units of the products, minus it in log2 units, sums
+    float m[NT], low[NT], l[NT], z[NT];
 #pragma unroll
     for (int half = 0; half < NT; ++half) {
       m[half] = -INFINITY;
-      l[half] = z[half] = 0.f;
+      low[half] = l[half] = z[half] = 0.f;
 #pragma unroll
       for (int j = 0; j < S::kMTiles; ++j)
 #pragma unroll
@@ -497,13 +514,12 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
 #pragma unroll
           for (int k = 0; k < 2; ++k) meta[g][k] = src[2 * c + k + 8 * g];
       }
-      const uint32_t bits = (uint32_t)valid >> (2 * c);
-      const bool on[2][2] = {{(bits & 1) != 0, (bits & 2) != 0}, {(bits & 0x100) != 0, (bits & 0x200) != 0}};
+      const uint32_t bits = (uint32_t)valid & 0xffffu;
       __syncwarp();
       const int ahead = tile + S::kStages * kWarps;
       uint32_t row;
-      const uint32_t ahead_bits = rows_of(ahead, next_page, &row);
-      next_page = page_of(ahead + kWarps);
+      const uint32_t ahead_bits = rows_of(ahead, next, &row);
+      next = page_of(ahead + kWarps);
       copy_keys(stage, row, ahead_bits);
       valid = valid >> 16 | (uint64_t)ahead_bits << (16 * (S::kStages - 1));
 
@@ -512,26 +528,30 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
 #pragma unroll
       for (int half = 0; half < NT; ++half) {
         float e[2][2];
-        float top = -INFINITY;
 #pragma unroll
         for (int g = 0; g < 2; ++g)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            float y = s[g][2 * half + k];
-            if constexpr (Q8)
-              y = fmaf(y, meta[g][k].x * (p.scale2 * 0x1p69f), meta[g][k].y * qsum[half]);
-            else
-              y *= p.scale2;
-            e[g][k] = on[g][k] ? y : -INFINITY;
-            top = fmaxf(top, e[g][k]);
+            e[g][k] = s[g][2 * half + k];
+            if constexpr (Q8) e[g][k] = fmaf(e[g][k], meta[g][k].x, meta[g][k].y * qsum[half]);
           }
+        if (bits != 0xffffu) {
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              if ((bits >> (2 * c + k + 8 * g) & 1) == 0) e[g][k] = -INFINITY;
+        }
+        float top = fmaxf(fmaxf(e[0][0], e[0][1]), fmaxf(e[1][0], e[1][1]));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const float high = fmaxf(m[half], top - M::kShift);
-        if (__any_sync(0xffffffffu, high > m[half] + M::kSlack)) {
+        const float high = fmaxf(m[half], top);
+        if (__any_sync(0xffffffffu, high > m[half] + p.slack)) {
           // a first maximum scales sums that are still zero
-          const float a = m[half] == -INFINITY ? 0.f : exp2_fast(m[half] - high);
+          const float next_low = high == -INFINITY ? 0.f : fmaf(-high, p.unit2, M::kShift);
+          const float a = m[half] == -INFINITY ? 0.f : exp2_fast(next_low - low[half]);
           m[half] = high;
+          low[half] = next_low;
           l[half] *= a;
           if constexpr (Q8) z[half] *= a;
           const float a0 = __shfl_sync(0xffffffffu, a, 8 * c), a1 = __shfl_sync(0xffffffffu, a, 8 * c + 4);
@@ -543,12 +563,11 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
             o[half][j][3] *= a1;
           }
         }
-        const float base = m[half] == -INFINITY ? 0.f : m[half];
 #pragma unroll
         for (int g = 0; g < 2; ++g)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            e[g][k] = exp2_fast(e[g][k] - base);
+            e[g][k] = exp2_fast(fmaf(e[g][k], p.unit2, low[half]));
             l[half] += e[g][k];
             if constexpr (Q8) {
               z[half] = fmaf(e[g][k], meta[g][k].w, z[half]);
@@ -558,7 +577,12 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           ph[half][g] = M::pack_down(e[g][0], e[g][1]);
-          pl[half][g] = M::pack(fmaxf(e[g][0] - M::lo(ph[half][g]), M::kTiny), fmaxf(e[g][1] - M::hi(ph[half][g]), M::kTiny));
+          float lo0 = e[g][0] - M::lo(ph[half][g]), lo1 = e[g][1] - M::hi(ph[half][g]);
+          if constexpr (!Q8) {  // codes are finite
+            lo0 = fmaxf(lo0, M::kTiny);
+            lo1 = fmaxf(lo1, M::kTiny);
+          }
+          pl[half][g] = M::pack(lo0, lo1);
           if (MODE == 0 && r >= 4) ph[half][g] = pl[half][g];
         }
       }
@@ -610,7 +634,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
         z[half] += __shfl_xor_sync(0xffffffffu, z[half], 2);
       }
       if (c == 0) {
-        sm[warp * kMaxRows + r + 8 * half] = m[half];
+        sm[warp * kMaxRows + r + 8 * half] = m[half] == -INFINITY ? -INFINITY : -low[half];
         sl[warp * kMaxRows + r + 8 * half] = l[half];
         if constexpr (Q8) sz[warp * kMaxRows + r + 8 * half] = z[half];
       }
@@ -647,9 +671,11 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
       }
     }
     __syncthreads();
+    const bool whole = t0 == 0 && t1 == tiles;
+    const int slot = 2 * me + (t0 == 0 ? 1 : 0);
     if (tid < rows) {
-      // factors of the warps' sums in the place of their maxima; the joint
-      // maximum and sum in sl[i], sl[kMaxRows + i]
+      // factors of the warps' sums in the place of their maxima, one over the
+      // joint sum in sl[i]
       float top = with_current ? sm[kWarps * kMaxRows + tid] : -INFINITY;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[w * kMaxRows + tid]);
@@ -666,35 +692,44 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
         sum += f;
         sm[kWarps * kMaxRows + tid] = f;
       }
-      sl[tid] = top;
-      sl[kMaxRows + tid] = sum;
+      const int mem = tid / p.group, li = sets.member[first + mem];
+      const int64_t to = (((int64_t)li * p.batch + b) * p.heads + h) * p.group + tid - mem * p.group;
+      out_at[tid] = whole ? to * D : ((int64_t)slot * p.rows + tid) * D;
+      cur_at[tid] = with_current ? p.cur_v.at(li, b, h) : nullptr;
+      sl[tid] = sum == 0.f ? 0.f : 1.f / sum;
+      if (!whole) p.stat[slot * p.rows + tid] = make_float2(top, sum);
+      else if (p.lse) p.lse[to] = lse_of(top, sum);
     }
     __syncthreads();
-    const bool whole = t0 == 0 && t1 == tiles;
-    const int slot = 2 * me + (t0 == 0 ? 1 : 0);
-    float* const part = p.part + (int64_t)slot * p.rows * D;
-    for (int idx = tid; idx < rows * D; idx += kThreads) {
-      const int i = idx / D, d = idx - i * D;
-      const int mem = i / p.group, li = sets.member[first + mem];
-      float acc = 0.f;
+    for (int idx = tid; idx < rows * (D / 4); idx += kThreads) {
+      const int i = idx / (D / 4), d = 4 * (idx - i * (D / 4));
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float f = sm[w * kMaxRows + i];
-        float y = so_of(w)[i * OS + d];
-        if constexpr (MODE == 0) y += so_of(w)[(i + 4) * OS + d];
-        if constexpr (Q8) y += sz[w * kMaxRows + i];
-        acc = fmaf(f, y, acc);
+        float4 y = *reinterpret_cast<const float4*>(so_of(w) + i * OS + d);
+        if constexpr (MODE == 0) {
+          const float4 lo = *reinterpret_cast<const float4*>(so_of(w) + (i + 4) * OS + d);
+          y = make_float4(y.x + lo.x, y.y + lo.y, y.z + lo.z, y.w + lo.w);
+        }
+        if constexpr (Q8) {
+          const float zero = sz[w * kMaxRows + i];
+          y = make_float4(y.x + zero, y.y + zero, y.z + zero, y.w + zero);
+        }
+        acc = make_float4(fmaf(f, y.x, acc.x), fmaf(f, y.y, acc.y), fmaf(f, y.z, acc.z), fmaf(f, y.w, acc.w));
       }
-      if (with_current) acc = fmaf(sm[kWarps * kMaxRows + i], M::lo(p.cur_v.at(li, b, h)[d]), acc);
-      const float top = sl[i], sum = sl[kMaxRows + i];
+      if (with_current) {
+        const float f = sm[kWarps * kMaxRows + i];
+        const uint2 w = *reinterpret_cast<const uint2*>(cur_at[i] + d);
+        acc = make_float4(fmaf(f, M::lo(w.x), acc.x), fmaf(f, M::hi(w.x), acc.y), fmaf(f, M::lo(w.y), acc.z), fmaf(f, M::hi(w.y), acc.w));
+      }
       if (whole) {
-        const int64_t to = (((int64_t)li * p.batch + b) * p.heads + h) * p.group + i - mem * p.group;
-        const float y = sum == 0.f ? 0.f : acc / sum;
-        p.out[to * D + d] = (uint16_t)(M::pack(y, y) & 0xffffu);
-        if (d == 0 && p.lse) p.lse[to] = lse_of(top, sum);
+        const float f = sl[i];
+        const bool none = f == 0.f;
+        *reinterpret_cast<uint2*>(p.out + out_at[i] + d) =
+            make_uint2(none ? 0u : M::pack(acc.x * f, acc.y * f), none ? 0u : M::pack(acc.z * f, acc.w * f));
       } else {
-        part[idx] = acc;
-        if (d == 0) p.stat[slot * p.rows + i] = make_float2(top, sum);
+        *reinterpret_cast<float4*>(p.part + out_at[i] + d) = acc;
       }
     }
     if (!whole && t0 == 0 && tid == 0) {
@@ -730,13 +765,13 @@ template <int D, int FMT>
 __global__ void __launch_bounds__(kJoinThreads)
 paged_join_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_constant__ Sets sets) {
   using M = Mma<FMT>;
-  constexpr int WARPS = kJoinThreads / 32, LANES = D / 4, GROUPS = kJoinThreads / LANES;
+  constexpr int WARPS = kJoinThreads / 32, LANES = D / 4, CHUNKS = D / 32, GROUPS = kJoinThreads / 8;
   constexpr int PER = (kMaxWorkers + kJoinThreads - 1) / kJoinThreads;
   __shared__ int2 split[kMaxWorkers];
   __shared__ uint16_t list[kMaxWorkers];
   __shared__ int counts[PER * WARPS];
   __shared__ float factor[kMaxWorkers], wm[WARPS], wl[WARPS];
-  __shared__ float4 sa[GROUPS][LANES];
+  __shared__ float4 sa[GROUPS][8 + 1];
   const int tid = threadIdx.x, lane = tid & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // the units of many parts, in order
@@ -809,8 +844,9 @@ paged_join_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_cons
     if (lane == 0 && p.lse) p.lse[to] = lse_of(top, sum);
   }
 
-  for (int it = blockIdx.x; it < n_list * p.rows; it += gridDim.x) {
-    const int at = it / p.rows, row = it - at * p.rows, i = list[at], more = split[i].y;
+  for (int it = blockIdx.x; it < n_list * p.rows * CHUNKS; it += gridDim.x) {
+    const int chunk = it % CHUNKS, item = it / CHUNKS;
+    const int at = item / p.rows, row = item - at * p.rows, i = list[at], more = split[i].y;
     const int64_t to = out_row(p, sets, split[i].x, row);
     if (to < 0) continue;
     float2 mine[PER];
@@ -839,11 +875,12 @@ paged_join_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_cons
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) wl[tid >> 5] = sum;
     __syncthreads();
-    const int lane4 = tid % LANES, group = tid / LANES;
+    const int lane4 = tid % 8, group = tid / 8;
+    float first = 0.f, second = 0.f;
     float4 acc4 = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
+#pragma unroll 4
     for (int k = group; k <= more; k += GROUPS) {
-      const float4 a = reinterpret_cast<const float4*>(p.part + ((int64_t)slot(i, k) * p.rows + row) * D)[lane4];
+      const float4 a = reinterpret_cast<const float4*>(p.part + ((int64_t)slot(i, k) * p.rows + row) * D)[8 * chunk + lane4];
       const float f = factor[k];
       acc4.x = fmaf(f, a.x, acc4.x);
       acc4.y = fmaf(f, a.y, acc4.y);
@@ -852,16 +889,25 @@ paged_join_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_cons
     }
     sa[group][lane4] = acc4;
     __syncthreads();
-    if (tid < D) {
+    // a warp sums two channels over the groups
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int d = 2 * (tid >> 5) + j;
       float acc = 0.f;
-      sum = 0.f;
 #pragma unroll
-      for (int g = 0; g < GROUPS; ++g) acc += reinterpret_cast<const float*>(sa[g])[tid];
+      for (int g = 0; g < GROUPS / 32; ++g) acc += reinterpret_cast<const float*>(sa[lane + 32 * g])[d];
 #pragma unroll
-      for (int w = 0; w < WARPS; ++w) sum += wl[w];
-      const float y = sum == 0.f ? 0.f : acc / sum;
-      p.out[to * D + tid] = (uint16_t)(M::pack(y, y) & 0xffffu);
-      if (tid == 0 && p.lse) p.lse[to] = lse_of(top, sum);
+      for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+      if (j == 0) first = acc;
+      else second = acc;
+    }
+    sum = lane < WARPS ? wl[lane] : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) {
+      const bool none = sum == 0.f;
+      reinterpret_cast<uint32_t*>(p.out + to * D + 32 * chunk)[tid >> 5] = none ? 0u : M::pack(first / sum, second / sum);
+      if (tid == 0 && chunk == 0 && p.lse) p.lse[to] = lse_of(top, sum);
     }
     __syncthreads();  // shared memory is free for the next item
   }
@@ -1008,9 +1054,13 @@ extern "C" loopkv_status loopkv_paged_decode(const loopkv_page_pool* pool, const
   p.group = desc->q_per_kv;
   p.max_pages = desc->max_pages;
   p.n_pages = pool->n_pages;
-  p.cell_rows = (int64_t)pool->n_pages * pool->n_kv_heads * pool->page_size;
+  p.cell_rows = (uint32_t)((int64_t)pool->n_pages * pool->n_kv_heads * pool->page_size);
   const float sm_scale = desc->sm_scale > 0.f ? desc->sm_scale : 1.0f / std::sqrt((float)pool->head_dim);
   p.scale2 = sm_scale * 1.4426950408889634f;
+  const bool q8 = pool->format == LOOPKV_PAGE_Q8;
+  p.unit2 = q8 ? p.scale2 * 0x1p69f : p.scale2;
+  // (finite: the first maximum is -infinity)
+  p.slack = std::min((pool->format == LOOPKV_PAGE_F16 ? Mma<LOOPKV_PAGE_F16>::kSlack : Mma<LOOPKV_PAGE_BF16>::kSlack) / p.unit2, 1e30f);
   p.div = PageDiv(pool->page_size);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return pool->head_dim == 64 ? launch_decode_dim<64>(pool->format, p, sets, s)
