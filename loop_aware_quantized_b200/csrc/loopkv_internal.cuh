@@ -4,6 +4,10 @@
 // nothing outside the library does.
 #pragma once
 
+#ifdef __CUDACC__
+#include <cuda_runtime.h>
+#endif
+
 #include <cstddef>
 #include <cstdint>
 
@@ -166,6 +170,33 @@ struct PageDiv {
   __host__ __device__ int page(int n) const { return (int)(((uint64_t)(uint32_t)n * mul) >> shift); }
   __host__ __device__ int pages(int n) const { return page(n + size - 1); }  // pages of n tokens
 };
+
+#ifdef __CUDACC__
+// Every kernel of the paged calls may be set up while the one before it in
+// its stream still runs (launch_early): it lets its own successor do so and
+// waits for its predecessor's end and writes before it reads or writes
+// anything.  A kernel that has ended has waited, so its successor is behind
+// all that came before it too.  Calls one after another: a page map 6.2 -> 4.9
+// us, one request's decode 16.5 -> 14.3 us.
+__device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... P>
+loopkv_status launch_early(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, void* stream,
+                           const P&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? LOOPKV_OK : LOOPKV_ERR_CUDA;
+}
+#endif
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool pool_ok(const loopkv_page_pool* p);  // paged_append.cu: argument checks of the paged calls

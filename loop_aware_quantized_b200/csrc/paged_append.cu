@@ -141,6 +141,8 @@ template <int D, bool Q8>
 __global__ void __launch_bounds__(kThreads)
 paged_append_kernel(const __grid_constant__ PagedAppendParams p, const __grid_constant__ CellList cells) {
   require_ieee_subnormals();
+  let_next_launch();
+  wait_for_previous();
   constexpr int LANES = Q8 ? D / 16 : D / 8;
   const uint32_t i = blockIdx.x * (uint32_t)(kThreads / LANES) + threadIdx.x / LANES;
   const int part = threadIdx.x % LANES;
@@ -255,10 +257,9 @@ extern "C" loopkv_status loopkv_paged_append(const loopkv_page_pool* pool, const
   p.cell_rows = (int64_t)pool->n_pages * pool->n_kv_heads * pool->page_size;
   p.div = PageDiv(pool->page_size);
   const dim3 grid((unsigned)blocks, (unsigned)stored);
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (pool->head_dim == 64 && q8) paged_append_kernel<64, true><<<grid, kThreads, 0, s>>>(p, cl);
-  else if (pool->head_dim == 64) paged_append_kernel<64, false><<<grid, kThreads, 0, s>>>(p, cl);
-  else if (q8) paged_append_kernel<128, true><<<grid, kThreads, 0, s>>>(p, cl);
-  else paged_append_kernel<128, false><<<grid, kThreads, 0, s>>>(p, cl);
-  return cudaGetLastError() == cudaSuccess ? LOOPKV_OK : LOOPKV_ERR_CUDA;
+  if (pool->head_dim == 64)
+    return q8 ? launch_early(paged_append_kernel<64, true>, grid, kThreads, 0, stream, p, cl)
+              : launch_early(paged_append_kernel<64, false>, grid, kThreads, 0, stream, p, cl);
+  return q8 ? launch_early(paged_append_kernel<128, true>, grid, kThreads, 0, stream, p, cl)
+            : launch_early(paged_append_kernel<128, false>, grid, kThreads, 0, stream, p, cl);
 }

@@ -178,6 +178,11 @@ __device__ __forceinline__ float lse_of(float top, float sum) {
   return sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
+// n / d, in 32 bits where they do (a 64-bit division is a hundred instructions)
+__device__ __forceinline__ uint64_t quotient(uint64_t n, uint32_t d) {
+  return (n >> 32) == 0 ? (uint32_t)n / d : n / d;
+}
+
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) {
   return __byte_perm(a, b, s);
 }
@@ -251,7 +256,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
   __shared__ int64_t out_at[kMaxRows];
   __shared__ const uint16_t* cur_at[kMaxRows];
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  let_next_launch();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
   uint8_t* const ring = smem + warp * S::kWarpBytes;
   const uint32_t ring_at = shared_at(ring);
@@ -266,6 +271,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
   const uint32_t page_rows = (uint32_t)p.heads * (uint32_t)p.div.size;  // (a pool's rows are numbered in 32 bits)
   uint32_t status = 0;
 
+  wait_for_previous();
   // Cost of a unit of every request: its tiles and its start and end.
   {
     const int per = (p.batch + kThreads - 1) / kThreads;
@@ -308,8 +314,10 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
   const int me = blockIdx.x;
   if (tid == 0) p.split[2 * me + 1] = 0;
   if (me >= workers) return;
-  const int64_t x1 = all * (me + 1) / workers;
-  int64_t x = all * me / workers;
+  // shares of all / workers, the first ones one longer
+  const uint64_t share = quotient((uint64_t)all, (uint32_t)workers), longer = (uint64_t)all - share * workers;
+  int64_t x = (int64_t)(share * me + min((uint64_t)me, longer));
+  const int64_t x1 = x + (int64_t)share + ((uint64_t)me < longer ? 1 : 0);
   int b = 0;
   {
     int lo = 0, hi = p.batch - 1;
@@ -323,7 +331,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
   while (x < x1) {
     const int cost = prefix[b + 1] - prefix[b];
     const int64_t rem = x - (int64_t)prefix[b] * per_request;
-    const int u = (int)(rem / cost), from = (int)(rem - (int64_t)u * cost);
+    const int u = (int)quotient((uint64_t)rem, (uint32_t)cost), from = (int)(rem - (int64_t)u * cost);
     const int set = u / p.heads, h = u - set * p.heads;
     const int upto = (int)min((int64_t)cost, from + (x1 - x));
     const int first = sets.first[set], rows = (sets.first[set + 1] - first) * p.group;
@@ -736,7 +744,8 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
       // the workers behind this one that hold the rest of the unit
       const int64_t last = x - upto + cost - 1;
       p.split[2 * me] = (set * p.batch + b) * p.heads + h;
-      p.split[2 * me + 1] = (int)(((last + 1) * workers - 1) / all) - me;
+      const uint64_t at = (uint64_t)last, head = longer * (share + 1);
+      p.split[2 * me + 1] = (int)(at < head ? at / (share + 1) : longer + (at - head) / share) - me;
     }
     __syncthreads();  // shared memory is free for the next unit
     if (x == (int64_t)prefix[b + 1] * per_request) ++b;
@@ -757,8 +766,7 @@ __device__ __forceinline__ int64_t out_row(const PagedDecodeParams& p, const Set
 // is one query row of such a unit.  Up to kFewParts parts are a warp's work;
 // more are a block's: all parts' maxima and sums at once, then their channels,
 // four to a thread, the parts dealt to groups of D / 4 threads, and the groups'
-// sums.  Launched while the decode still runs (every block waits for its end
-// before it reads).  What bounds it: four dependent round trips to L2.  With
+// sums.  What bounds it: four dependent round trips to L2.  With
 // one thread a channel and a running maximum over the parts, 2 units of 300
 // parts took 17 us; with a block per worker and row, 2000 rows of 2 parts 8 us.
 template <int D, int FMT>
@@ -773,7 +781,8 @@ paged_join_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_cons
   __shared__ float factor[kMaxWorkers], wm[WARPS], wl[WARPS];
   __shared__ float4 sa[GROUPS][8 + 1];
   const int tid = threadIdx.x, lane = tid & 31;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  let_next_launch();
+  wait_for_previous();
   // the units of many parts, in order
   bool many[PER];
   uint32_t ballot[PER];
@@ -926,18 +935,8 @@ loopkv_status launch_decode_kernel(PagedDecodeParams p, const Sets& sets, cudaSt
   const auto kernel = paged_decode_kernel<D, FMT, MODE, FLAT>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return LOOPKV_ERR_CUDA;
-  kernel<<<p.workers, kThreads, smem, stream>>>(p, sets);
-  if (cudaGetLastError() != cudaSuccess) return LOOPKV_ERR_CUDA;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(kJoinBlocks, 1, 1);
-  cfg.blockDim = dim3(kJoinThreads, 1, 1);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, FMT>, p, sets) == cudaSuccess ? LOOPKV_OK : LOOPKV_ERR_CUDA;
+  const loopkv_status rc = launch_early(kernel, dim3((unsigned)p.workers), kThreads, smem, stream, p, sets);
+  return rc != LOOPKV_OK ? rc : launch_early(paged_join_kernel<D, FMT>, dim3(kJoinBlocks), kJoinThreads, 0, stream, p, sets);
 }
 
 template <int D, int FMT, int MODE>

@@ -119,7 +119,10 @@ __global__ void __launch_bounds__(kPageThreads) page_map_kernel(const __grid_con
   extern __shared__ int mem[];
   __shared__ long long warp_sums[32];
   const Shared sh = shared_arrays(mem, p.batch);
-  if (p.expand) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // The finishing launch reads the lengths before it waits, so the expanding one
+  // lets it start only when what came before is done.
+  if (p.expand) wait_for_previous();
+  let_next_launch();
   const int tid = threadIdx.x, threads = blockDim.x, per = (p.batch + threads - 1) / threads;
   uint32_t status = 0;
 
@@ -242,7 +245,7 @@ __global__ void __launch_bounds__(kPageThreads) page_map_kernel(const __grid_con
   }
   if (!p.finish) return;
   if (lane == 0) warp_sums[tid >> 5] = taken;
-  if (!p.expand) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!p.expand) wait_for_previous();
   __syncthreads();  // every thread has read the lengths and the free count
 #pragma unroll
   for (int k = 0; k < kPerThread; ++k) {
@@ -261,7 +264,10 @@ page_release_kernel(const __grid_constant__ PageParams p) {
   extern __shared__ int mem[];
   __shared__ long long warp_sums[32];
   const Shared sh = shared_arrays(mem, p.batch);
-  if (p.expand) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // The finishing launch reads the lengths before it waits, so the expanding one
+  // lets it start only when what came before is done.
+  if (p.expand) wait_for_previous();
+  let_next_launch();
   const int tid = threadIdx.x, threads = blockDim.x, per = (p.batch + threads - 1) / threads;
   uint32_t status = 0;
 
@@ -348,7 +354,7 @@ page_release_kernel(const __grid_constant__ PageParams p) {
   }
   if (status && p.status) atomicOr(p.status, status);
   if (!p.finish) return;
-  if (!p.expand) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!p.expand) wait_for_previous();
   __syncthreads();  // every thread has read the lengths and the free count
 #pragma unroll
   for (int k = 0; k < kPerThread; ++k) {
@@ -370,33 +376,20 @@ bool page_args_ok(int32_t batch, int32_t page_size, int32_t max_pages, int32_t n
 // work: rows (map) or pages (release) the call may have to expand, at most.
 // A short call is one launch of one CTA: at 4096 rows that takes as long as the two
 // launches of a long one.
-template <typename Kernel>
-loopkv_status launch_pages(Kernel kernel, PageParams p, long long work, void* stream) {
+loopkv_status launch_pages(void (*kernel)(PageParams), PageParams p, long long work, void* stream) {
   const size_t smem = sizeof(int) * (3 * (size_t)p.batch + 1);
   if (smem > 40 * 1024 &&  // 48 KB less the static part need no asking
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return LOOPKV_ERR_CUDA;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   p.expand = true;
   p.finish = work <= kShortWork;
-  const int few = p.finish && work <= kUnroll * kFewThreads && p.batch <= kFewThreads;
+  const bool few = p.finish && work <= kUnroll * kFewThreads && p.batch <= kFewThreads;
   const long long ctas = p.finish ? 1 : std::min<long long>((work + kPageThreads - 1) / kPageThreads, kSms);
-  kernel<<<(unsigned)ctas, few ? kFewThreads : kPageThreads, smem, s>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return LOOPKV_ERR_CUDA;
-  if (p.finish) return LOOPKV_OK;
+  const loopkv_status rc = launch_early(kernel, dim3((unsigned)ctas), few ? kFewThreads : kPageThreads, smem, stream, p);
+  if (rc != LOOPKV_OK || p.finish) return rc;
   p.expand = false;
   p.finish = true;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(1, 1, 1);
-  cfg.blockDim = dim3(kPageThreads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? LOOPKV_OK : LOOPKV_ERR_CUDA;
+  return launch_early(kernel, dim3(1), kPageThreads, smem, stream, p);
 }
 
 }  // namespace

@@ -546,6 +546,65 @@ def test_decode_on_another_stream(dev):
     assert (got[0] == want[0]).all() and (got[1] == want[1]).all()
 
 
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_one_after_another_see_each_others_results(dev, captured):
+    # kernels are set up while their predecessors run: long in-place maps and releases, appends and
+    # decodes back to back, torch's kernels between them, against the same calls one at a time
+    import torch
+    from loop_aware_quantized_b200 import page_map, page_release, paged_append, paged_decode
+    rng = np.random.default_rng(4)
+    B, ps, width, rows, heads, dim = 300, 4, 40, 6000, 2, 64
+    n_pages = B * width
+    new = [np.where(rng.random(B) < 0.7, rng.integers(0, 25, B), 0) for _ in range(4)]
+    g = torch.Generator(device=dev).manual_seed(0)
+    rand = lambda *sh: torch.randn(sh, generator=g, device=dev).to(torch.bfloat16)  # noqa: E731
+    k, v, q = rand(1, rows, heads, dim), rand(1, rows, heads, dim), rand(1, B, heads, dim)
+    adds = [ints(x, dev) for x in new]
+
+    def state():
+        z = lambda n: ints(np.zeros(n), dev)  # noqa: E731
+        return dict(len=z(B), table=ints(np.full((B, width), -1), dev), free=ints(rng2.permutation(n_pages), dev),
+                    count=ints([n_pages], dev), slots=z(rows), starts=z(B + 1), cut=z(B), status=z(1),
+                    kp=torch.zeros((1, n_pages, heads, ps, dim), dtype=torch.bfloat16, device=dev),
+                    vp=torch.zeros((1, n_pages, heads, ps, dim), dtype=torch.bfloat16, device=dev),
+                    outs=[torch.zeros_like(q) for _ in adds])
+
+    def run(s, between=lambda: None):
+        for i, add in enumerate(adds):
+            page_map(s["len"], add, s["table"], s["free"], s["count"], ps, s["slots"], s["starts"], status=s["status"])
+            between()
+            paged_append([0], k, v, s["slots"], s["kp"], s["vp"], status=s["status"])
+            between()
+            paged_decode([0], q, s["kp"], s["vp"], s["table"], s["len"], out=s["outs"][i], status=s["status"])
+            between()
+            torch.div(s["len"], 2, rounding_mode="floor", out=s["cut"])
+            page_release(s["len"], s["cut"], s["table"], s["free"], s["count"], ps, status=s["status"])
+            between()
+            page_release(s["len"], s["cut"], s["table"], s["free"], s["count"], ps, status=s["status"])
+            between()
+
+    rng2 = np.random.default_rng(5)
+    want = state()
+    run(want, torch.cuda.synchronize)
+    for _ in range(10):
+        rng2 = np.random.default_rng(5)
+        got = state()
+        if captured:
+            side = torch.cuda.Stream(dev)
+            side.wait_stream(torch.cuda.current_stream())
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=side):
+                run(got)
+            graph.replay()
+        else:
+            run(got)
+        torch.cuda.synchronize()
+        for name in ("len", "table", "free", "count", "slots", "starts", "status", "kp", "vp"):
+            assert (got[name] == want[name]).all(), name
+        assert all((a == b).all() for a, b in zip(got["outs"], want["outs"]))
+    assert int(want["status"]) == 0 and sum((o != 0).any() for o in want["outs"]) == 4
+
+
 def test_every_way_of_calling_gives_the_same(dev):
     # the short way (current stream) and the long one (a stream given, a tensor subclass, cells as
     # a tuple or range), lists and arrays of cells, outputs given or made
