@@ -64,11 +64,11 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kSms = 148;
-constexpr int kMaxWorkers = kSms * 4;
-constexpr int kTile = 16;            // tokens of a warp's step
-constexpr int kMinCost = 2 * kWarps;  // cost a worker takes at least
-constexpr int kUnitCost = 24;         // tiles that a unit's start and end are worth
-constexpr int kEmptyCost = 2;         // and a unit without tokens, which is only written
+constexpr int kMaxWorkers = kSms * 3;
+constexpr int kPage = 16;             // pages of a multiple of this are FLAT (below)
+constexpr int kMinTokens = 128;       // what a worker takes at least
+constexpr int kUnitTokens = 384;      // tokens that a unit's start and end are worth
+constexpr int kEmptyTokens = 32;      // and a unit without tokens, which is only written
 constexpr int kMaxRows = LOOPKV_MAX_PAGED_GROUP;  // query rows of a set
 constexpr int kJoinThreads = 512;
 constexpr int kJoinBlocks = 2 * kSms;
@@ -222,14 +222,24 @@ struct Shape {
   static constexpr int kRowBytes = kQ8 ? D : 2 * D;
   static constexpr int kPieces = kRowBytes / 16;
   static constexpr int kRowsPerCopy = 32 / kPieces;    // rows one instruction of a warp copies
-  static constexpr int kCopies = kTile / kRowsPerCopy;
+  // Tokens of a tile, a warp's step.  What a step costs besides its products
+  // (waits, rows, maxima: some 100 instructions) is halved by 32, which took 8-bit
+  // pages of 1024 ragged requests from 266 to 186 us; two such tiles of 16 bits x 128
+  // channels do not fit shared memory, and the registers of 8 bits x 128
+  // channels x 16 rows do not hold them (187 us with 16 tokens, 266 with 32).
+  static constexpr int kTok = kRowBytes == 256 || (kQ8 && D == 128 && MODE == 2) ? 16 : 32;
+  static constexpr int kCopies = kTok / kRowsPerCopy;
+  static constexpr int kGroups = kTok / 8;
+  static constexpr uint32_t kAll = kTok == 32 ? 0xffffffffu : 0xffffu;
   static constexpr int kSteps = D / 16;        // contraction steps of the scores
   static constexpr int kMTiles = D / 16;       // 16-channel tiles of the output
-  static constexpr int kRowsBytes = kTile * kRowBytes;
-  static constexpr int kTileBytes = 2 * kRowsBytes + (kQ8 ? 16 * kTile : 0);
-  static constexpr int kStages = kTileBytes > 8000 ? 2 : (kTileBytes > 4000 ? 3 : 4);
+  static constexpr int kRowsBytes = kTok * kRowBytes;
+  static constexpr int kTileBytes = 2 * kRowsBytes + (kQ8 ? 16 * kTok : 0);
+  static constexpr int kStages = kTileBytes > 8000 ? 2 : 3;
   static constexpr int kWarpBytes = kStages * kTileBytes;
-  static constexpr int kCtasPerSm = (kTileBytes > 8000 || (MODE == 2 && D == 128)) ? 3 : 4;
+  static constexpr int kCtasPerSm = 3;
+  // costs in tiles
+  static constexpr int kUnitCost = kUnitTokens / kTok, kEmptyCost = kEmptyTokens / kTok, kMinCost = kMinTokens / kTok;
   static constexpr int kWorkers = kSms * kCtasPerSm;
   static __device__ __forceinline__ int swizzle(int t) { return kPieces == 4 ? (t >> 1) & 3 : t & 7; }
 };
@@ -284,7 +294,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
         status |= LOOPKV_PAGE_BAD_LENGTH;
         n = 0;
       }
-      const int t = n == 0 ? kEmptyCost : kUnitCost + (n + kTile - 1) / kTile;
+      const int t = n == 0 ? S::kEmptyCost : S::kUnitCost + (n + S::kTok - 1) / S::kTok;
       prefix[b + 1] = t;
       sum += t;
     }
@@ -309,7 +319,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
   }
   const int per_request = p.n_sets * p.heads;
   const int64_t all = (int64_t)prefix[p.batch] * per_request;
-  const int64_t want = (all + kMinCost - 1) / kMinCost;
+  const int64_t want = (all + S::kMinCost - 1) / S::kMinCost;
   const int workers = (int)(want < p.workers ? want : p.workers);
   const int me = blockIdx.x;
   if (tid == 0) p.split[2 * me + 1] = 0;
@@ -349,22 +359,23 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
       if (x == (int64_t)prefix[b + 1] * per_request) ++b;
       continue;
     }
-    // position i of a unit's cost is its tile i - kUnitCost
-    const int tiles = cost - kUnitCost, t0 = max(0, from - kUnitCost), t1 = upto - kUnitCost;
+    // position i of a unit's cost is its tile i - S::kUnitCost
+    const int tiles = cost - S::kUnitCost, t0 = max(0, from - S::kUnitCost), t1 = upto - S::kUnitCost;
     if (t1 <= 0) break;  // the share ends before the unit's first tile
     const bool current = (sets.cell[set] & kCurrentBit) != 0 && n > 0;
     const uint32_t cell_row = (uint32_t)(sets.cell[set] & ~kCurrentBit) * p.cell_rows + (uint32_t)(h * p.div.size);
     const int np = current ? n - 1 : n;  // tokens read from pages
 
-    // The page of token (lane & 15) of a tile (FLAT: of its first token), loaded
-    // a step before the tile is copied.  A tile is then a row (FLAT: the first
-    // one; else the lane's token's) and a bit per token to be read.
+    // The page of the lane's token of a tile (FLAT: of the first token of the
+    // lane's half of it), loaded a step before the tile is copied.  A tile is then
+    // a row of every lane's token (FLAT: of every half's first one) and a bit per
+    // token to be read.
     const int32_t* const entry = p.table + (int64_t)b * p.max_pages;
     struct Next {
       int page, off;
     };
     auto page_of = [&](int tile) -> Next {
-      const int pos = tile * kTile + (FLAT ? 0 : lane & 15);
+      const int pos = tile * S::kTok + (lane & (FLAT ? S::kTok - 16 : S::kTok - 1));
       if (tile >= t1 || pos >= np) return {INT_MIN, 0};
       const int j = p.div.page(pos);
       return {__ldg(entry + j), pos - j * p.div.size};
@@ -373,24 +384,28 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
       const bool good = at.page >= 0 && at.page < p.n_pages;
       if (!good && at.page != INT_MIN) status |= LOOPKV_PAGE_BAD_PAGE;
       *row = good ? cell_row + (uint32_t)at.page * page_rows + (uint32_t)at.off : 0u;
-      if (FLAT) return good ? (1u << min(kTile, np - tile * kTile)) - 1u : 0u;
-      return __ballot_sync(0xffffffffu, good) & 0xffffu;
+      const uint32_t found = __ballot_sync(0xffffffffu, good) & S::kAll;
+      const int left = np - tile * S::kTok;
+      return FLAT && left < S::kTok ? found & ((1u << max(left, 0)) - 1u) : found;
     };
     auto copy_rows = [&](uint32_t at, const uint8_t* src, uint32_t row, uint32_t bits) {
       at += copy_row * S::kRowBytes;
       src += 16 * piece;
       auto dst = [&](int t) { return at + t * S::kRowBytes + ((piece ^ S::swizzle(t + copy_row)) << 4); };
       if constexpr (FLAT) {
-        src += ((uint64_t)row + copy_row) * S::kRowBytes;
-        if (bits == 0xffffu) {
+        const uint8_t* half[S::kTok / 16];
 #pragma unroll
-          for (int i = 0; i < S::kCopies; ++i)
-            copy16(dst(i * S::kRowsPerCopy), src + i * S::kRowsPerCopy * S::kRowBytes);
+        for (int h = 0; h < S::kTok / 16; ++h)
+          half[h] = src + ((uint64_t)(S::kTok == 16 ? row : __shfl_sync(0xffffffffu, row, 16 * h)) + copy_row) * S::kRowBytes;
+        auto from = [&](int t) { return half[t / 16] + t % 16 * S::kRowBytes; };
+        if (bits == S::kAll) {
+#pragma unroll
+          for (int i = 0; i < S::kCopies; ++i) copy16(dst(i * S::kRowsPerCopy), from(i * S::kRowsPerCopy));
         } else {
           bits >>= copy_row;
 #pragma unroll
           for (int i = 0; i < S::kCopies; ++i)
-            copy16(dst(i * S::kRowsPerCopy), src + i * S::kRowsPerCopy * S::kRowBytes, (bits >> (i * S::kRowsPerCopy) & 1) != 0);
+            copy16(dst(i * S::kRowsPerCopy), from(i * S::kRowsPerCopy), (bits >> (i * S::kRowsPerCopy) & 1) != 0);
         }
       } else {
         bits >>= copy_row;
@@ -404,8 +419,8 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
     auto copy_keys = [&](int stage, uint32_t row, uint32_t bits) {
       const uint32_t at = ring_at + stage * S::kTileBytes;
       copy_rows(at, p.k, row, bits);
-      if (Q8 && lane < kTile)
-        copy16(at + 2 * S::kRowsBytes + 16 * lane, reinterpret_cast<const uint8_t*>(p.meta + (row + (FLAT ? (uint64_t)lane : 0))), (bits >> lane & 1) != 0);
+      if (Q8 && lane < S::kTok)
+        copy16(at + 2 * S::kRowsBytes + 16 * lane, reinterpret_cast<const uint8_t*>(p.meta + (row + (FLAT ? (uint64_t)(lane & 15) : 0))), (bits >> lane & 1) != 0);
       copy_commit();
     };
     auto copy_values = [&](int stage, uint32_t row, uint32_t bits) {
@@ -413,8 +428,8 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
       copy_commit();
     };
 
-    // The first tiles' copies; valid holds 16 bits a stage, this step's lowest.
-    uint64_t valid = 0;
+    // The first tiles' copies; valid[0] is this step's.
+    uint32_t valid[S::kStages];
     Next next;
     {
       Next pages[S::kStages];
@@ -427,7 +442,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
         const uint32_t bits = rows_of(t0 + warp + s * kWarps, pages[s], &row);
         copy_keys(s, row, bits);
         copy_values(s, row, bits);
-        valid |= (uint64_t)bits << (16 * s);
+        valid[s] = bits;
       }
     }
 
@@ -494,63 +509,68 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
       copy_wait<2 * S::kStages - 1>();
 
       // Scores.
-      float s[2][4];
+      float s[S::kGroups][4];
 #pragma unroll
-      for (int g = 0; g < 2; ++g) s[g][0] = s[g][1] = s[g][2] = s[g][3] = 0.f;
+      for (int g = 0; g < S::kGroups; ++g) s[g][0] = s[g][1] = s[g][2] = s[g][3] = 0.f;
       auto score = [&](int g, int ks, uint32_t b0, uint32_t b1) {
         if constexpr (MODE == 2) M::run(s[g], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], b0, b1);
         else M::run(s[g], qa[ks][0], 0u, qa[ks][1], 0u, b0, b1);
       };
 #pragma unroll
-      for (int i = 0; i < S::kPieces / 2; ++i) {
-        uint32_t w[4];  // tokens 0-7: pieces 2 i, 2 i + 1; tokens 8-15: the same
-        ldsm(w, (keys + k_at) ^ (i << 5));
-        if constexpr (Q8) {
+      for (int i = 0; i < S::kPieces / 2; ++i)
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            score(k >> 1, 2 * i + (k & 1), prmt(w[k], 0, 0x4140), prmt(w[k], 0, 0x4342));
-        } else {
-          score(0, i, w[0], w[1]);
-          score(1, i, w[2], w[3]);
+        for (int h = 0; h < S::kGroups; h += 2) {
+          uint32_t w[4];  // tokens 0-7 of the half: pieces 2 i, 2 i + 1; tokens 8-15: the same
+          ldsm(w, ((keys + k_at) ^ (i << 5)) + 8 * h * S::kRowBytes);
+          if constexpr (Q8) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              score(h + (k >> 1), 2 * i + (k & 1), prmt(w[k], 0, 0x4140), prmt(w[k], 0, 0x4342));
+          } else {
+            score(h, i, w[0], w[1]);
+            score(h + 1, i, w[2], w[3]);
+          }
         }
-      }
-      float4 meta[2][2];
+      float4 meta[S::kGroups][2];
       if constexpr (Q8) {
         const float4* src = reinterpret_cast<const float4*>(ring + stage * S::kTileBytes + 2 * S::kRowsBytes);
 #pragma unroll
-        for (int g = 0; g < 2; ++g)
+        for (int g = 0; g < S::kGroups; ++g)
 #pragma unroll
           for (int k = 0; k < 2; ++k) meta[g][k] = src[2 * c + k + 8 * g];
       }
-      const uint32_t bits = (uint32_t)valid & 0xffffu;
+      const uint32_t bits = valid[0];
       __syncwarp();
       const int ahead = tile + S::kStages * kWarps;
       uint32_t row;
       const uint32_t ahead_bits = rows_of(ahead, next, &row);
       next = page_of(ahead + kWarps);
       copy_keys(stage, row, ahead_bits);
-      valid = valid >> 16 | (uint64_t)ahead_bits << (16 * (S::kStages - 1));
+#pragma unroll
+      for (int i = 0; i + 1 < S::kStages; ++i) valid[i] = valid[i + 1];
+      valid[S::kStages - 1] = ahead_bits;
 
-      // Weights, 4 tokens of a query row per lane.
-      uint32_t ph[NT][2], pl[NT][2];
+      // Weights, two tokens of every 8 of a query row per lane.
+      uint32_t ph[NT][S::kGroups], pl[NT][S::kGroups];
 #pragma unroll
       for (int half = 0; half < NT; ++half) {
-        float e[2][2];
+        float e[S::kGroups][2], top = -INFINITY;
 #pragma unroll
-        for (int g = 0; g < 2; ++g)
+        for (int g = 0; g < S::kGroups; ++g)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             e[g][k] = s[g][2 * half + k];
             if constexpr (Q8) e[g][k] = fmaf(e[g][k], meta[g][k].x, meta[g][k].y * qsum[half]);
           }
-        if (bits != 0xffffu) {
+        if (bits != S::kAll) {
 #pragma unroll
-          for (int g = 0; g < 2; ++g)
+          for (int g = 0; g < S::kGroups; ++g)
 #pragma unroll
             for (int k = 0; k < 2; ++k)
               if ((bits >> (2 * c + k + 8 * g) & 1) == 0) e[g][k] = -INFINITY;
         }
-        float top = fmaxf(fmaxf(e[0][0], e[0][1]), fmaxf(e[1][0], e[1][1]));
+#pragma unroll
+        for (int g = 0; g < S::kGroups; ++g) top = fmaxf(top, fmaxf(e[g][0], e[g][1]));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const float high = fmaxf(m[half], top);
@@ -572,7 +592,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
           }
         }
 #pragma unroll
-        for (int g = 0; g < 2; ++g)
+        for (int g = 0; g < S::kGroups; ++g)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             e[g][k] = exp2_fast(fmaf(e[g][k], p.unit2, low[half]));
@@ -583,7 +603,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
             }
           }
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
+        for (int g = 0; g < S::kGroups; ++g) {
           ph[half][g] = M::pack_down(e[g][0], e[g][1]);
           float lo0 = e[g][0] - M::lo(ph[half][g]), lo1 = e[g][1] - M::hi(ph[half][g]);
           if constexpr (!Q8) {  // codes are finite
@@ -598,32 +618,34 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
       // out^T += V^T p^T
       copy_wait<2 * S::kStages - 1>();
 #pragma unroll
-      for (int i = 0; i < S::kPieces / 2; ++i) {
-        uint32_t w[4];
-        ldsm_trans(w, (values + v_at) ^ (i << 5));
-        if constexpr (!Q8) {
-          // tile i: rows r, r + 8 are channels 16 i + r, 16 i + 8 + r
+      for (int i = 0; i < S::kPieces / 2; ++i)
 #pragma unroll
-          for (int half = 0; half < NT; ++half) {
-            M::run(o[half][i], w[0], w[1], w[2], w[3], ph[half][0], ph[half][1]);
-            if constexpr (MODE != 0) M::run(o[half][i], w[0], w[1], w[2], w[3], pl[half][0], pl[half][1]);
-          }
-        } else {
-          // tile j: rows r, r + 8 are channels 16 j + 2 r, 16 j + 2 r + 1, the
-          // low and the high bytes of a pair
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int j = 2 * i + k;
-            const uint32_t a0 = prmt(w[2 * k], 0, 0x4240), a1 = prmt(w[2 * k], 0, 0x4341);
-            const uint32_t a2 = prmt(w[2 * k + 1], 0, 0x4240), a3 = prmt(w[2 * k + 1], 0, 0x4341);
+        for (int h = 0; h < S::kGroups; h += 2) {
+          uint32_t w[4];
+          ldsm_trans(w, ((values + v_at) ^ (i << 5)) + 8 * h * S::kRowBytes);
+          if constexpr (!Q8) {
+            // tile i: rows r, r + 8 are channels 16 i + r, 16 i + 8 + r
 #pragma unroll
             for (int half = 0; half < NT; ++half) {
-              M::run(o[half][j], a0, a1, a2, a3, ph[half][0], ph[half][1]);
-              if constexpr (MODE != 0) M::run(o[half][j], a0, a1, a2, a3, pl[half][0], pl[half][1]);
+              M::run(o[half][i], w[0], w[1], w[2], w[3], ph[half][h], ph[half][h + 1]);
+              if constexpr (MODE != 0) M::run(o[half][i], w[0], w[1], w[2], w[3], pl[half][h], pl[half][h + 1]);
+            }
+          } else {
+            // tile j: rows r, r + 8 are channels 16 j + 2 r, 16 j + 2 r + 1, the
+            // low and the high bytes of a pair
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int j = 2 * i + k;
+              const uint32_t a0 = prmt(w[2 * k], 0, 0x4240), a1 = prmt(w[2 * k], 0, 0x4341);
+              const uint32_t a2 = prmt(w[2 * k + 1], 0, 0x4240), a3 = prmt(w[2 * k + 1], 0, 0x4341);
+#pragma unroll
+              for (int half = 0; half < NT; ++half) {
+                M::run(o[half][j], a0, a1, a2, a3, ph[half][h], ph[half][h + 1]);
+                if constexpr (MODE != 0) M::run(o[half][j], a0, a1, a2, a3, pl[half][h], pl[half][h + 1]);
+              }
             }
           }
         }
-      }
       __syncwarp();
       copy_values(stage, row, ahead_bits);
       stage = stage + 1 == S::kStages ? 0 : stage + 1;
@@ -796,8 +818,8 @@ paged_join_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_cons
     if (lane == 0) counts[j * WARPS + (tid >> 5)] = __popc(ballot[j]);
   }
   __syncthreads();
-  static_assert(PER * WARPS == 32, "a count a lane");
-  const int count = counts[lane];
+  static_assert(PER * WARPS <= 32, "a count a lane");
+  const int count = lane < PER * WARPS ? counts[lane] : 0;
   int upto = count;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -941,7 +963,7 @@ loopkv_status launch_decode_kernel(PagedDecodeParams p, const Sets& sets, cudaSt
 
 template <int D, int FMT, int MODE>
 loopkv_status launch_decode_mode(const PagedDecodeParams& p, const Sets& sets, cudaStream_t stream) {
-  return p.div.size % kTile == 0 ? launch_decode_kernel<D, FMT, MODE, true>(p, sets, stream)
+  return p.div.size % kPage == 0 ? launch_decode_kernel<D, FMT, MODE, true>(p, sets, stream)
                                  : launch_decode_kernel<D, FMT, MODE, false>(p, sets, stream);
 }
 
