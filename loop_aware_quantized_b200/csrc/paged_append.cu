@@ -141,7 +141,6 @@ template <int D, bool Q8>
 __global__ void __launch_bounds__(kThreads)
 paged_append_kernel(const __grid_constant__ PagedAppendParams p, const __grid_constant__ CellList cells) {
   require_ieee_subnormals();
-  let_next_launch();
   wait_for_previous();
   constexpr int LANES = Q8 ? D / 16 : D / 8;
   const uint32_t i = blockIdx.x * (uint32_t)(kThreads / LANES) + threadIdx.x / LANES;

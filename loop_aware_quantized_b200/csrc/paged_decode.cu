@@ -70,9 +70,10 @@ constexpr int kMinTokens = 128;       // what a worker takes at least
 constexpr int kUnitTokens = 384;      // tokens that a unit's start and end are worth
 constexpr int kEmptyTokens = 32;      // and a unit without tokens, which is only written
 constexpr int kMaxRows = LOOPKV_MAX_PAGED_GROUP;  // query rows of a set
-constexpr int kJoinThreads = 512;
-constexpr int kJoinBlocks = 2 * kSms;
+constexpr int kJoinThreads = 256;
 constexpr int kFewParts = 16;         // a warp joins fewer continuations than this
+constexpr int kJoinOwners = (kMaxWorkers + kFewParts - 1) / kFewParts;
+constexpr int kJoinSpread = 32;       // blocks at most that share an owner's rows and channels
 constexpr int kCurrentBit = 1 << 30;  // in a set's cell: the last token is in cur_k / cur_v
 
 struct RowView {
@@ -266,7 +267,6 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
   __shared__ int64_t out_at[kMaxRows];
   __shared__ const uint16_t* cur_at[kMaxRows];
 
-  let_next_launch();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
   uint8_t* const ring = smem + warp * S::kWarpBytes;
   const uint32_t ring_at = shared_at(ring);
@@ -281,6 +281,10 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
   const uint32_t page_rows = (uint32_t)p.heads * (uint32_t)p.div.size;  // (a pool's rows are numbered in 32 bits)
   uint32_t status = 0;
 
+  {  // the constants' first lines, while the kernel before this one ends
+    const int warm = sets.cell[0] + sets.first[1] + sets.member[0] + p.n_sets + p.group;
+    asm volatile("" ::"r"(warm));
+  }
   wait_for_previous();
   // Cost of a unit of every request: its tiles and its start and end.
   {
@@ -428,14 +432,36 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
       copy_commit();
     };
 
-    // The first tiles' copies; valid[0] is this step's.
-    uint32_t valid[S::kStages];
+    // The first tiles' pages, the query fragments (asked for before the tiles: at
+    // the start of a call every SM's copies are in the way of what comes behind
+    // them), and the tiles' copies; valid[0] is this step's.
+    uint32_t qa[S::kSteps][MODE == 2 ? 4 : 2], valid[S::kStages];
     Next next;
     {
       Next pages[S::kStages];
 #pragma unroll
       for (int s = 0; s < S::kStages; ++s) pages[s] = page_of(t0 + warp + s * kWarps);
       next = page_of(t0 + warp + S::kStages * kWarps);
+#pragma unroll
+      for (int half = 0; half < NT; ++half) {
+        const int row = MODE == 0 ? (r & 3) : r + 8 * half;
+        const bool on = row < rows;
+        const int mem = on ? row / p.group : 0;
+        const uint16_t* src = p.q.at(sets.member[first + mem], b, h * p.group + (on ? row - mem * p.group : 0));
+#pragma unroll
+        for (int i = 0; i < S::kSteps; ++i) {
+          uint2 w = make_uint2(0, 0);
+          if (on) {
+            if constexpr (!Q8)
+              w = make_uint2(__ldg(reinterpret_cast<const uint32_t*>(src + 16 * i + 2 * c)),
+                             __ldg(reinterpret_cast<const uint32_t*>(src + 16 * i + 8 + 2 * c)));
+            else  // a lane's 4 codes of a 16-byte piece are channels 4 c ..
+              w = __ldg(reinterpret_cast<const uint2*>(src + 16 * i + 4 * c));
+          }
+          qa[i][MODE == 2 ? half : 0] = w.x;
+          qa[i][MODE == 2 ? 2 + half : 1] = w.y;
+        }
+      }
 #pragma unroll
       for (int s = 0; s < S::kStages; ++s) {
         uint32_t row;
@@ -446,48 +472,24 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
       }
     }
 
-    // Query fragments.
-    uint32_t qa[S::kSteps][MODE == 2 ? 4 : 2];
     float qsum[NT];
 #pragma unroll
     for (int half = 0; half < NT; ++half) {
-      const int row = MODE == 0 ? (r & 3) : r + 8 * half;
-      const bool on = row < rows;
-      const int mem = on ? row / p.group : 0;
-      const uint16_t* src = p.q.at(sets.member[first + mem], b, h * p.group + (on ? row - mem * p.group : 0));
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < S::kSteps; ++i) {
-        uint32_t w0 = 0, w1 = 0;
-        if constexpr (!Q8) {
-          if (on) {
-            w0 = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * i + 2 * c));
-            w1 = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * i + 8 + 2 * c));
-          }
-        } else {
-          // a lane's 4 codes of a 16-byte piece are channels 4 c ..
-          if (on) {
-            const uint2 w = __ldg(reinterpret_cast<const uint2*>(src + 16 * i + 4 * c));
-            w0 = w.x;
-            w1 = w.y;
-          }
-          sum += (M::lo(w0) + M::hi(w0)) + (M::lo(w1) + M::hi(w1));
-          w0 = M::pack(M::lo(w0) * 0x1p64f, M::hi(w0) * 0x1p64f);
-          w1 = M::pack(M::lo(w1) * 0x1p64f, M::hi(w1) * 0x1p64f);
-        }
-        if constexpr (MODE == 2) {
-          qa[i][half] = w0;
-          qa[i][2 + half] = w1;
-        } else {
-          qa[i][0] = w0;
-          qa[i][1] = w1;
-        }
-      }
+      qsum[half] = 0.f;
       if constexpr (Q8) {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < S::kSteps; ++i)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            uint32_t& w = qa[i][MODE == 2 ? 2 * k + half : k];
+            sum += M::lo(w) + M::hi(w);
+            w = M::pack(M::lo(w) * 0x1p64f, M::hi(w) * 0x1p64f);
+          }
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        qsum[half] = sum * 0x1p-69f;
       }
-      qsum[half] = sum * 0x1p-69f;
     }
 
     float o[NT][S::kMTiles][4];
@@ -784,63 +786,126 @@ __device__ __forceinline__ int64_t out_row(const PagedDecodeParams& p, const Set
 }
 
 // Join the parts of the units that a worker i began and did not end: its own
-// (slot 2 i + 1) and those of the workers behind it (slots 2 (i + k)).  An item
-// is one query row of such a unit.  Up to kFewParts parts are a warp's work;
-// more are a block's: all parts' maxima and sums at once, then their channels,
-// four to a thread, the parts dealt to groups of D / 4 threads, and the groups'
-// sums.  What bounds it: four dependent round trips to L2.  With
-// one thread a channel and a running maximum over the parts, 2 units of 300
-// parts took 17 us; with a block per worker and row, 2000 rows of 2 parts 8 us.
+// (slot 2 i + 1) and those of the workers behind it (slots 2 (i + k)).  What is
+// joined is one query row of such a unit; with up to kFewParts parts it is a
+// warp's work.  More are a block's, 32 channels at a time: all parts' maxima and
+// sums and four channels of up to four parts to a thread at once, then the
+// rest.  Owners of units of that many parts are kFewParts workers apart and more,
+// so every kFewParts workers have one at most, found by a look at their
+// entries.  What bounds it: two dependent round trips to L2 and, as in any
+// short kernel, its start.  With a running maximum over the parts and one thread a
+// channel 2 units of 300 parts took 17 us, with a block per worker and row 2000
+// rows of 2 parts took 8.
 template <int D, int FMT>
 __global__ void __launch_bounds__(kJoinThreads)
 paged_join_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_constant__ Sets sets) {
   using M = Mma<FMT>;
   constexpr int WARPS = kJoinThreads / 32, LANES = D / 4, CHUNKS = D / 32, GROUPS = kJoinThreads / 8;
-  constexpr int PER = (kMaxWorkers + kJoinThreads - 1) / kJoinThreads;
-  __shared__ int2 split[kMaxWorkers];
-  __shared__ uint16_t list[kMaxWorkers];
-  __shared__ int counts[PER * WARPS];
+  constexpr int PER = (kMaxWorkers + kJoinThreads - 1) / kJoinThreads, FIRST = 4;
+  static_assert(GROUPS == 32, "a group a lane");
   __shared__ float factor[kMaxWorkers], wm[WARPS], wl[WARPS];
   __shared__ float4 sa[GROUPS][8 + 1];
-  const int tid = threadIdx.x, lane = tid & 31;
-  let_next_launch();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   wait_for_previous();
-  // the units of many parts, in order
-  bool many[PER];
-  uint32_t ballot[PER];
-#pragma unroll
-  for (int j = 0; j < PER; ++j) {
-    const int i = tid + j * kJoinThreads;
-    const int2 mine = i < p.workers ? reinterpret_cast<const int2*>(p.split)[i] : make_int2(0, 0);
-    if (i < p.workers) split[i] = mine;
-    many[j] = mine.y >= kFewParts;
-    ballot[j] = __ballot_sync(0xffffffffu, many[j]);
-    if (lane == 0) counts[j * WARPS + (tid >> 5)] = __popc(ballot[j]);
-  }
-  __syncthreads();
-  static_assert(PER * WARPS <= 32, "a count a lane");
-  const int count = lane < PER * WARPS ? counts[lane] : 0;
-  int upto = count;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += y;
-  }
-  const int n_list = __shfl_sync(0xffffffffu, upto, 31);
-#pragma unroll
-  for (int j = 0; j < PER; ++j) {
-    const int before = __shfl_sync(0xffffffffu, upto - count, j * WARPS + (tid >> 5));
-    if (many[j]) list[before + __popc(ballot[j] & ((1u << lane) - 1u))] = (uint16_t)(tid + j * kJoinThreads);
-  }
-  __syncthreads();
+  const int2* const split = reinterpret_cast<const int2*>(p.split);
   auto slot = [&](int i, int k) { return k == 0 ? 2 * i + 1 : 2 * (i + k); };
+  auto part = [&](int i, int k, int row) {
+    return reinterpret_cast<const float4*>(p.part + ((int64_t)slot(i, k) * p.rows + row) * D);
+  };
+  auto add = [](float4& acc, float f, const float4& a) {
+    acc = make_float4(fmaf(f, a.x, acc.x), fmaf(f, a.y, acc.y), fmaf(f, a.z, acc.z), fmaf(f, a.w, acc.w));
+  };
+  auto store = [&](int64_t at, const float4& acc, float sum) {
+    const bool none = sum == 0.f;
+    *reinterpret_cast<uint2*>(p.out + at) = make_uint2(none ? 0u : M::pack(acc.x / sum, acc.y / sum),
+                                                       none ? 0u : M::pack(acc.z / sum, acc.w / sum));
+  };
 
-  for (int it = blockIdx.x * WARPS + (tid >> 5); it < p.workers * p.rows; it += gridDim.x * WARPS) {
-    const int i = it / p.rows, row = it - i * p.rows, more = split[i].y;
+  const int few = blockIdx.x % kJoinOwners, w0 = few * kFewParts + lane;
+  const int2 seen = lane < kFewParts && w0 < p.workers ? split[w0] : make_int2(0, 0);
+  const uint32_t many = __ballot_sync(0xffffffffu, seen.y >= kFewParts);
+  if (many != 0) {
+    const int from = __ffs(many) - 1, i = few * kFewParts + from;
+    const int unit = __shfl_sync(0xffffffffu, seen.x, from), more = __shfl_sync(0xffffffffu, seen.y, from);
+    for (int it = blockIdx.x / kJoinOwners; it < p.rows * CHUNKS; it += gridDim.x / kJoinOwners) {
+      const int row = it / CHUNKS, chunk = it % CHUNKS;
+      const int64_t to = out_row(p, sets, unit, row);
+      if (to < 0) continue;
+      const int lane4 = tid % 8, group = tid / 8;
+      float2 mine[PER];
+      float4 a[FIRST];
+      float top = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        const int k = tid + j * kJoinThreads;
+        mine[j] = k <= more ? p.stat[slot(i, k) * p.rows + row] : make_float2(-INFINITY, 0.f);
+      }
+#pragma unroll
+      for (int j = 0; j < FIRST; ++j) {
+        const int k = group + j * GROUPS;
+        a[j] = k <= more ? part(i, k, row)[8 * chunk + lane4] : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int j = 0; j < PER; ++j) top = fmaxf(top, mine[j].x);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if (lane == 0) wm[warp] = top;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) top = fmaxf(top, wm[w]);
+      const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        const int k = tid + j * kJoinThreads;
+        const float f = exp2_fast(mine[j].x - base);
+        if (k <= more) factor[k] = f;
+        sum = fmaf(f, mine[j].y, sum);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane == 0) wl[warp] = sum;
+      __syncthreads();
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < FIRST; ++j)
+        if (group + j * GROUPS <= more) add(acc, factor[group + j * GROUPS], a[j]);
+#pragma unroll 4
+      for (int k = group + FIRST * GROUPS; k <= more; k += GROUPS) add(acc, factor[k], part(i, k, row)[8 * chunk + lane4]);
+      sa[group][lane4] = acc;
+      __syncthreads();
+      acc = sa[lane][warp];  // four channels of a group: a warp sums them over the groups
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        acc.x += __shfl_xor_sync(0xffffffffu, acc.x, o);
+        acc.y += __shfl_xor_sync(0xffffffffu, acc.y, o);
+        acc.z += __shfl_xor_sync(0xffffffffu, acc.z, o);
+        acc.w += __shfl_xor_sync(0xffffffffu, acc.w, o);
+      }
+      sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) sum += wl[w];
+      if (lane == 0) store(to * D + 32 * chunk + 4 * warp, acc, sum);
+      if (tid == 0 && chunk == 0 && p.lse) p.lse[to] = lse_of(top, sum);
+      __syncthreads();  // shared memory is free for the next row
+    }
+  }
+
+  for (int it = blockIdx.x * WARPS + warp; it < p.workers * p.rows; it += gridDim.x * WARPS) {
+    const int i = it / p.rows, row = it - i * p.rows;
+    const int2 own = split[i];
+    const int more = own.y;
     if (more == 0 || more >= kFewParts) continue;
-    const int64_t to = out_row(p, sets, split[i].x, row);
+    const int64_t to = out_row(p, sets, own.x, row);
     if (to < 0) continue;
+    // 32 / LANES parts at a time, the first ones before the factors are known
+    const int lane4 = lane % LANES, k1 = lane / LANES;
+    float4 a[FIRST];
     const float2 mine = lane <= more ? p.stat[slot(i, lane) * p.rows + row] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+    for (int j = 0; j < FIRST; ++j) {
+      const int k = k1 + j * (32 / LANES);
+      a[j] = k <= more ? part(i, k, row)[lane4] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
     float top = mine.x;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -849,16 +914,16 @@ paged_join_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_cons
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int k0 = 0; k0 <= more; k0 += 32 / LANES) {
-      const int k = k0 + lane / LANES;
+#pragma unroll
+    for (int j = 0; j < FIRST; ++j) {
+      const int k = k1 + j * (32 / LANES);
       const float g = __shfl_sync(0xffffffffu, f, k);
-      if (k > more) continue;
-      const float4 a = reinterpret_cast<const float4*>(p.part + ((int64_t)slot(i, k) * p.rows + row) * D)[lane % LANES];
-      acc.x = fmaf(g, a.x, acc.x);
-      acc.y = fmaf(g, a.y, acc.y);
-      acc.z = fmaf(g, a.z, acc.z);
-      acc.w = fmaf(g, a.w, acc.w);
+      if (k <= more) add(acc, g, a[j]);
+    }
+    for (int k0 = FIRST * (32 / LANES); k0 <= more; k0 += 32 / LANES) {
+      const int k = k0 + k1;
+      const float g = __shfl_sync(0xffffffffu, f, k);
+      if (k <= more) add(acc, g, part(i, k, row)[lane4]);
     }
 #pragma unroll
     for (int o = 16; o >= LANES; o >>= 1) {
@@ -867,80 +932,8 @@ paged_join_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_cons
       acc.z += __shfl_xor_sync(0xffffffffu, acc.z, o);
       acc.w += __shfl_xor_sync(0xffffffffu, acc.w, o);
     }
-    const bool none = sum == 0.f;
-    if (lane < LANES)
-      reinterpret_cast<uint2*>(p.out + to * D)[lane] =
-          make_uint2(M::pack(none ? 0.f : acc.x / sum, none ? 0.f : acc.y / sum),
-                     M::pack(none ? 0.f : acc.z / sum, none ? 0.f : acc.w / sum));
+    if (lane < LANES) store(to * D + 4 * lane, acc, sum);
     if (lane == 0 && p.lse) p.lse[to] = lse_of(top, sum);
-  }
-
-  for (int it = blockIdx.x; it < n_list * p.rows * CHUNKS; it += gridDim.x) {
-    const int chunk = it % CHUNKS, item = it / CHUNKS;
-    const int at = item / p.rows, row = item - at * p.rows, i = list[at], more = split[i].y;
-    const int64_t to = out_row(p, sets, split[i].x, row);
-    if (to < 0) continue;
-    float2 mine[PER];
-    float top = -INFINITY, sum = 0.f;
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      const int k = tid + j * kJoinThreads;
-      mine[j] = k <= more ? p.stat[slot(i, k) * p.rows + row] : make_float2(-INFINITY, 0.f);
-      top = fmaxf(top, mine[j].x);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0) wm[tid >> 5] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) top = fmaxf(top, wm[w]);
-    const float base = top == -INFINITY ? 0.f : top;
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      const int k = tid + j * kJoinThreads;
-      const float f = exp2_fast(mine[j].x - base);
-      if (k <= more) factor[k] = f;
-      sum = fmaf(f, mine[j].y, sum);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) wl[tid >> 5] = sum;
-    __syncthreads();
-    const int lane4 = tid % 8, group = tid / 8;
-    float first = 0.f, second = 0.f;
-    float4 acc4 = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = group; k <= more; k += GROUPS) {
-      const float4 a = reinterpret_cast<const float4*>(p.part + ((int64_t)slot(i, k) * p.rows + row) * D)[8 * chunk + lane4];
-      const float f = factor[k];
-      acc4.x = fmaf(f, a.x, acc4.x);
-      acc4.y = fmaf(f, a.y, acc4.y);
-      acc4.z = fmaf(f, a.z, acc4.z);
-      acc4.w = fmaf(f, a.w, acc4.w);
-    }
-    sa[group][lane4] = acc4;
-    __syncthreads();
-    // a warp sums two channels over the groups
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int d = 2 * (tid >> 5) + j;
-      float acc = 0.f;
-#pragma unroll
-      for (int g = 0; g < GROUPS / 32; ++g) acc += reinterpret_cast<const float*>(sa[lane + 32 * g])[d];
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-      if (j == 0) first = acc;
-      else second = acc;
-    }
-    sum = lane < WARPS ? wl[lane] : 0.f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) {
-      const bool none = sum == 0.f;
-      reinterpret_cast<uint32_t*>(p.out + to * D + 32 * chunk)[tid >> 5] = none ? 0u : M::pack(first / sum, second / sum);
-      if (tid == 0 && chunk == 0 && p.lse) p.lse[to] = lse_of(top, sum);
-    }
-    __syncthreads();  // shared memory is free for the next item
   }
 }
 
@@ -958,7 +951,7 @@ loopkv_status launch_decode_kernel(PagedDecodeParams p, const Sets& sets, cudaSt
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return LOOPKV_ERR_CUDA;
   const loopkv_status rc = launch_early(kernel, dim3((unsigned)p.workers), kThreads, smem, stream, p, sets);
-  return rc != LOOPKV_OK ? rc : launch_early(paged_join_kernel<D, FMT>, dim3(kJoinBlocks), kJoinThreads, 0, stream, p, sets);
+  return rc != LOOPKV_OK ? rc : launch_early(paged_join_kernel<D, FMT>, dim3((unsigned)(kJoinOwners * std::min(kJoinSpread, p.rows * (D / 32)))), kJoinThreads, 0, stream, p, sets);
 }
 
 template <int D, int FMT, int MODE>

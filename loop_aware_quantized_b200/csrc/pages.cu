@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kPageThreads) page_map_kernel(const __grid_con
   // The finishing launch reads the lengths before it waits, so the expanding one
   // lets it start only when what came before is done.
   if (p.expand) wait_for_previous();
-  let_next_launch();
+  if (!p.finish) let_next_launch();
   const int tid = threadIdx.x, threads = blockDim.x, per = (p.batch + threads - 1) / threads;
   uint32_t status = 0;
 
@@ -267,7 +267,7 @@ page_release_kernel(const __grid_constant__ PageParams p) {
   // The finishing launch reads the lengths before it waits, so the expanding one
   // lets it start only when what came before is done.
   if (p.expand) wait_for_previous();
-  let_next_launch();
+  if (!p.finish) let_next_launch();
   const int tid = threadIdx.x, threads = blockDim.x, per = (p.batch + threads - 1) / threads;
   uint32_t status = 0;
 
