@@ -5,12 +5,12 @@
 // any IEEE implementation of the same steps gives the same codes).
 //
 // A thread moves 16 bytes of a key vector and the same 16 of the value vector
-// (Q8: two such pieces of each, half a vector apart, so that what is done once
-// per vector is shared by more values); a vector's threads sit in one warp, so
-// its minimum and maximum are a few shuffles.  What bounds it: memory.  Each
-// byte is read once and written once; a vector is 128 or 256 contiguous bytes
-// on both sides.  A division per value took more than twice as long as the
-// bytes (2 cells of 16384 rows, 16 heads of 128: 175 us): see codes8.
+// (Q8: four such pieces of each, a quarter vector apart); a vector's threads sit
+// in one warp, so its minimum and maximum are a few shuffles.  What bounds it:
+// memory.  Each byte is read once and written once; a vector is 128 or 256
+// contiguous bytes on both sides.  36865 rows of 16 heads of 128 in fp16: 94 us, 6.27
+// TB/s.  With a division per value Q8 took more than twice as long as its bytes
+// (2 cells of 16384 rows: 175 us, now 65): see codes8.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -23,7 +23,12 @@
 namespace loopkv {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+// 16-byte pieces of a key vector and of a value vector that a Q8 thread does:
+// what is done once per vector (scale, reciprocal, addresses) is shared by so
+// many more values (2: 78 us, 4: 65 us of 63 that the bytes take; 2 cells of 16384 rows,
+// 16 heads of 128).
+constexpr int kPieces = 4;
 
 struct PagedAppendParams {
   const uint16_t* k;
@@ -116,15 +121,18 @@ __device__ __forceinline__ uint2 codes8(const uint4& x, const Quantizer& z) {
   return make_uint2(pack4(c[0], c[1], c[2], c[3]), pack4(c[4], c[5], c[6], c[7]));
 }
 
-// The smallest and the negated largest of 16 bf16 values (two pieces), as a pair.
-__device__ __forceinline__ __nv_bfloat162 extremes(const uint4& x, const uint4& y) {
-  const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-  __nv_bfloat162 mn = *reinterpret_cast<const __nv_bfloat162*>(&w[0]), mx = mn;
+// The smallest and the negated largest of a thread's bf16 values, as a pair.
+__device__ __forceinline__ __nv_bfloat162 extremes(const uint4 (&x)[kPieces]) {
+  __nv_bfloat162 mn = *reinterpret_cast<const __nv_bfloat162*>(&x[0].x), mx = mn;
 #pragma unroll
-  for (int i = 1; i < 8; ++i) {
-    const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(&w[i]);
-    mn = __hmin2(mn, v);
-    mx = __hmax2(mx, v);
+  for (int j = 0; j < kPieces; ++j) {
+    const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(&w[i]);
+      mn = __hmin2(mn, v);
+      mx = __hmax2(mx, v);
+    }
   }
   return __halves2bfloat162(__hmin(__low2bfloat16(mn), __high2bfloat16(mn)),
                             __hneg(__hmax(__low2bfloat16(mx), __high2bfloat16(mx))));
@@ -142,7 +150,7 @@ __global__ void __launch_bounds__(kThreads)
 paged_append_kernel(const __grid_constant__ PagedAppendParams p, const __grid_constant__ CellList cells) {
   require_ieee_subnormals();
   wait_for_previous();
-  constexpr int LANES = Q8 ? D / 16 : D / 8;
+  constexpr int LANES = Q8 ? D / (8 * kPieces) : D / 8;
   const uint32_t i = blockIdx.x * (uint32_t)(kThreads / LANES) + threadIdx.x / LANES;
   const int part = threadIdx.x % LANES;
   const bool in = i < p.vectors;
@@ -159,21 +167,21 @@ paged_append_kernel(const __grid_constant__ PagedAppendParams p, const __grid_co
   const int64_t at = cells.cell[blockIdx.y] * p.cell_rows +
                      ((int64_t)page * p.heads + head) * p.div.size + off;
   if constexpr (Q8) {
-    uint4 k[2], v[2];
-    k[0] = k[1] = v[0] = v[1] = make_uint4(0, 0, 0, 0);
-    if (slot >= 0) {
+    uint4 k[kPieces], v[kPieces];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        k[j] = *reinterpret_cast<const uint4*>(ks + j * (D / 2));
-        v[j] = *reinterpret_cast<const uint4*>(vs + j * (D / 2));
+    for (int j = 0; j < kPieces; ++j) {
+      k[j] = v[j] = make_uint4(0, 0, 0, 0);
+      if (slot >= 0) {
+        k[j] = *reinterpret_cast<const uint4*>(ks + j * (D / kPieces));
+        v[j] = *reinterpret_cast<const uint4*>(vs + j * (D / kPieces));
       }
     }
-    const Quantizer kz = quantizer<LANES>(extremes(k[0], k[1])), vz = quantizer<LANES>(extremes(v[0], v[1]));
+    const Quantizer kz = quantizer<LANES>(extremes(k)), vz = quantizer<LANES>(extremes(v));
     if (slot < 0) return;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      *reinterpret_cast<uint2*>(p.kp + at * D + part * 8 + j * (D / 2)) = codes8(k[j], kz);
-      *reinterpret_cast<uint2*>(p.vp + at * D + part * 8 + j * (D / 2)) = codes8(v[j], vz);
+    for (int j = 0; j < kPieces; ++j) {
+      *reinterpret_cast<uint2*>(p.kp + at * D + part * 8 + j * (D / kPieces)) = codes8(k[j], kz);
+      *reinterpret_cast<uint2*>(p.vp + at * D + part * 8 + j * (D / kPieces)) = codes8(v[j], vz);
     }
     if (part == 0) p.meta[at] = make_float4(kz.scale, kz.zero(), vz.scale, vz.zero());
   } else {
@@ -234,7 +242,7 @@ extern "C" loopkv_status loopkv_paged_append(const loopkv_page_pool* pool, const
   if (stored == 0) return LOOPKV_OK;
   const int64_t vectors = (int64_t)n_rows * pool->n_kv_heads;
   const bool q8 = pool->format == LOOPKV_PAGE_Q8;
-  const int64_t blocks = (vectors * (pool->head_dim / (q8 ? 16 : 8)) + kThreads - 1) / kThreads;
+  const int64_t blocks = (vectors * (pool->head_dim / (q8 ? 8 * kPieces : 8)) + kThreads - 1) / kThreads;
   if (vectors >= (1LL << 32) - kThreads || blocks >= (1LL << 31)) return LOOPKV_ERR_UNSUPPORTED;
   PagedAppendParams p{};
   p.k = static_cast<const uint16_t*>(k->data);
