@@ -10,13 +10,16 @@
 //   page_release  pages i of the free list's new end: request b with
 //                 start_b <= i, its table entry.
 // Every CTA reads the lengths and does the (short) prefix sum for itself, so
-// CTAs need not wait for one another.  A short call is one CTA, which stores
-// the new lengths and free count behind a block barrier.  A long one is a grid
-// that expands, and one more CTA, launched while the grid runs, that repeats
-// the prefix sum, waits for the grid's end and stores them: behind that
-// nothing reads the old ones, which is what lets them be updated in place, and
-// the call be captured and replayed.  What bounds it: the launch and two
-// dependent memory round trips (lengths, then free list or table).
+// CTAs need not wait for one another, and the first one stores the new lengths
+// and free count.  Where these take the old ones' place, nothing may read the
+// old ones any more: a short call is one CTA and a block barrier; a long one is a
+// grid that expands, and one more CTA, launched while the grid runs, that
+// repeats the prefix sum, waits for the grid's end and stores (a million rows:
+// 9.1 us, 8.5 where the outputs lie elsewhere and the grid does it all).  So
+// lengths are updated in place, and a call can be captured and replayed.  What
+// bounds it: the launch and two dependent memory round trips (lengths, then
+// free list or table); 32 requests' step takes 3.9 us, releases of a small batch
+// 3.5, half a million pages given back 6.7.
 
 #include <cuda_runtime.h>
 
@@ -243,7 +246,7 @@ __global__ void __launch_bounds__(kPageThreads) page_map_kernel(const __grid_con
     const long long y = __shfl_xor_sync(0xffffffffu, taken, o);
     taken = y > taken ? y : taken;
   }
-  if (!p.finish) return;
+  if (!p.finish || blockIdx.x != 0) return;
   if (lane == 0) warp_sums[tid >> 5] = taken;
   if (!p.expand) wait_for_previous();
   __syncthreads();  // every thread has read the lengths and the free count
@@ -353,7 +356,7 @@ page_release_kernel(const __grid_constant__ PageParams p) {
     }
   }
   if (status && p.status) atomicOr(p.status, status);
-  if (!p.finish) return;
+  if (!p.finish || blockIdx.x != 0) return;
   if (!p.expand) wait_for_previous();
   __syncthreads();  // every thread has read the lengths and the free count
 #pragma unroll
@@ -373,19 +376,19 @@ bool page_args_ok(int32_t batch, int32_t page_size, int32_t max_pages, int32_t n
          (long long)n_pages * page_size < (1LL << 31);
 }
 
-// work: rows (map) or pages (release) the call may have to expand, at most.
-// A short call is one launch of one CTA: at 4096 rows that takes as long as the two
-// launches of a long one.
-loopkv_status launch_pages(void (*kernel)(PageParams), PageParams p, long long work, void* stream) {
+// work: rows (map) or pages (release) the call may have to expand, at most;
+// threads: of a call of one CTA; in_place: an output takes an input's place.
+loopkv_status launch_pages(void (*kernel)(PageParams), PageParams p, long long work, int threads, bool in_place,
+                           void* stream) {
   const size_t smem = sizeof(int) * (3 * (size_t)p.batch + 1);
   if (smem > 40 * 1024 &&  // 48 KB less the static part need no asking
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return LOOPKV_ERR_CUDA;
+  const bool one = work <= kShortWork;
   p.expand = true;
-  p.finish = work <= kShortWork;
-  const bool few = p.finish && work <= kUnroll * kFewThreads && p.batch <= kFewThreads;
-  const long long ctas = p.finish ? 1 : std::min<long long>((work + kPageThreads - 1) / kPageThreads, kSms);
-  const loopkv_status rc = launch_early(kernel, dim3((unsigned)ctas), few ? kFewThreads : kPageThreads, smem, stream, p);
+  p.finish = one || !in_place;
+  const long long ctas = one ? 1 : std::min<long long>((work + kPageThreads - 1) / kPageThreads, kSms);
+  const loopkv_status rc = launch_early(kernel, dim3((unsigned)ctas), one ? threads : kPageThreads, smem, stream, p);
   if (rc != LOOPKV_OK || p.finish) return rc;
   p.expand = false;
   p.finish = true;
@@ -428,7 +431,8 @@ extern "C" loopkv_status loopkv_page_map(int32_t batch, int32_t page_size, int32
   p.n_pages = n_pages;
   p.n_rows = n_rows;
   p.div = PageDiv(page_size);
-  return launch_pages(page_map_kernel, p, n_rows, stream);
+  const int threads = n_rows <= kUnroll * kFewThreads && batch <= kFewThreads ? kFewThreads : kPageThreads;
+  return launch_pages(page_map_kernel, p, n_rows, threads, d_len_out == d_len || d_free_count_out == d_free_count, stream);
 }
 
 extern "C" loopkv_status loopkv_page_release(int32_t batch, int32_t page_size, int32_t max_pages,
@@ -457,5 +461,7 @@ extern "C" loopkv_status loopkv_page_release(int32_t batch, int32_t page_size, i
   p.n_pages = n_pages;
   p.div = PageDiv(page_size);
   const long long most = std::min<long long>((long long)batch * max_pages, n_pages);
-  return launch_pages(page_release_kernel, p, most, stream);
+  // (few of the pages that requests may hold are given back by one call)
+  return launch_pages(page_release_kernel, p, most, batch <= kFewThreads ? kFewThreads : kPageThreads,
+                      d_len_out == d_len || d_len_out == d_new_len || d_free_count_out == d_free_count, stream);
 }
