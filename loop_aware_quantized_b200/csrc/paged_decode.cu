@@ -103,7 +103,7 @@ struct PagedDecodeParams {
   float scale2;       // sm_scale * log2(e)
   float unit2;        // the same for a score as the products give it (Q8: times 2^69)
   float slack;        // kSlack in those units
-  PageDiv div;
+  PageDiv div, by_heads, by_group, by_batch;
 };
 
 // Listed cells that read the same pool cell in the same way, in sets of at
@@ -346,7 +346,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
     const int cost = prefix[b + 1] - prefix[b];
     const int64_t rem = x - (int64_t)prefix[b] * per_request;
     const int u = (int)quotient((uint64_t)rem, (uint32_t)cost), from = (int)(rem - (int64_t)u * cost);
-    const int set = u / p.heads, h = u - set * p.heads;
+    const int set = p.by_heads.page(u), h = u - set * p.heads;
     const int upto = (int)min((int64_t)cost, from + (x1 - x));
     const int first = sets.first[set], rows = (sets.first[set + 1] - first) * p.group;
     int n = p.len[b];
@@ -355,7 +355,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
     if (n == 0) {
       // written by the worker whose share has its first position
       for (int i = from == 0 ? tid : rows * (D / 8); i < rows * (D / 8); i += kThreads) {
-        const int row = i / (D / 8), mem = row / p.group, li = sets.member[first + mem];
+        const int row = i / (D / 8), mem = p.by_group.page(row), li = sets.member[first + mem];
         const int64_t at = (((int64_t)li * p.batch + b) * p.heads + h) * p.group + row - mem * p.group;
         reinterpret_cast<uint4*>(p.out + at * D)[i - row * (D / 8)] = make_uint4(0, 0, 0, 0);
         if (i == row * (D / 8) && p.lse) p.lse[at] = -INFINITY;
@@ -446,7 +446,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
       for (int half = 0; half < NT; ++half) {
         const int row = MODE == 0 ? (r & 3) : r + 8 * half;
         const bool on = row < rows;
-        const int mem = on ? row / p.group : 0;
+        const int mem = on ? p.by_group.page(row) : 0;
         const uint16_t* src = p.q.at(sets.member[first + mem], b, h * p.group + (on ? row - mem * p.group : 0));
 #pragma unroll
         for (int i = 0; i < S::kSteps; ++i) {
@@ -687,7 +687,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
     const bool with_current = current && t1 == tiles;
     if (with_current) {
       for (int i = warp; i < rows; i += kWarps) {
-        const int mem = i / p.group, li = sets.member[first + mem];
+        const int mem = p.by_group.page(i), li = sets.member[first + mem];
         const uint16_t* q = p.q.at(li, b, h * p.group + i - mem * p.group);
         const uint16_t* k = p.cur_k.at(li, b, h);
         float dot = 0.f;
@@ -724,7 +724,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
         sum += f;
         sm[kWarps * kMaxRows + tid] = f;
       }
-      const int mem = tid / p.group, li = sets.member[first + mem];
+      const int mem = p.by_group.page(tid), li = sets.member[first + mem];
       const int64_t to = (((int64_t)li * p.batch + b) * p.heads + h) * p.group + tid - mem * p.group;
       out_at[tid] = whole ? to * D : ((int64_t)slot * p.rows + tid) * D;
       cur_at[tid] = with_current ? p.cur_v.at(li, b, h) : nullptr;
@@ -779,8 +779,8 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
 
 // Where a row of a unit goes.
 __device__ __forceinline__ int64_t out_row(const PagedDecodeParams& p, const Sets& sets, int unit, int row) {
-  const int h = unit % p.heads, sb = unit / p.heads, set = sb / p.batch, b = sb - set * p.batch;
-  const int first = sets.first[set], mem = row / p.group;
+  const int sb = p.by_heads.page(unit), h = unit - sb * p.heads, set = p.by_batch.page(sb), b = sb - set * p.batch;
+  const int first = sets.first[set], mem = p.by_group.page(row);
   if (first + mem >= sets.first[set + 1]) return -1;  // a smaller set
   return (((int64_t)sets.member[first + mem] * p.batch + b) * p.heads + h) * p.group + row - mem * p.group;
 }
@@ -1076,6 +1076,9 @@ extern "C" loopkv_status loopkv_paged_decode(const loopkv_page_pool* pool, const
   // (finite: the first maximum is -infinity)
   p.slack = std::min((pool->format == LOOPKV_PAGE_F16 ? Mma<LOOPKV_PAGE_F16>::kSlack : Mma<LOOPKV_PAGE_BF16>::kSlack) / p.unit2, 1e30f);
   p.div = PageDiv(pool->page_size);
+  p.by_heads = PageDiv(p.heads);
+  p.by_group = PageDiv(p.group);
+  p.by_batch = PageDiv(p.batch);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return pool->head_dim == 64 ? launch_decode_dim<64>(pool->format, p, sets, s)
                               : launch_decode_dim<128>(pool->format, p, sets, s);
