@@ -39,14 +39,18 @@ constexpr int kSms = 148;
 constexpr int kShortWork = 4096;  // rows or pages of a one-CTA call
 constexpr long long kSatRows = 0x7fffffffLL;
 
-// Exclusive prefix sum over the block's threads; *total gets the sum.
-__device__ __forceinline__ long long block_scan(long long x, long long* warp_sums, long long* total) {
+// Exclusive prefix sum over the block's threads; *total gets the sum.  any: the
+// warp has requests (the others only need the barriers; a million rows of 256
+// requests: 8.5 -> 8.2 us).
+__device__ __forceinline__ long long block_scan(long long x, bool any, long long* warp_sums, long long* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   long long inc = x;
+  if (any) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += y;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
   }
   __syncthreads();  // the last scan's readers are done
   if (lane == 31) warp_sums[warp] = inc;
@@ -127,6 +131,7 @@ __global__ void __launch_bounds__(kPageThreads) page_map_kernel(const __grid_con
   if (p.expand) wait_for_previous();
   if (!p.finish) let_next_launch();
   const int tid = threadIdx.x, threads = blockDim.x, per = (p.batch + threads - 1) / threads;
+  const bool any = (tid & ~31) * per < p.batch;
   uint32_t status = 0;
 
   int len[kPerThread], add[kPerThread];
@@ -145,7 +150,7 @@ __global__ void __launch_bounds__(kPageThreads) page_map_kernel(const __grid_con
     free_count = 0;
   }
   long long all_rows, all_need;
-  long long start = block_scan(rows, warp_sums, &all_rows);
+  long long start = block_scan(rows, any, warp_sums, &all_rows);
   const long long capacity = (long long)p.max_pages * p.div.size;
   int need[kPerThread];
   long long sum = 0;
@@ -169,7 +174,7 @@ __global__ void __launch_bounds__(kPageThreads) page_map_kernel(const __grid_con
       sum += need[k];
     }
   }
-  long long before = block_scan(sum, warp_sums, &all_need);
+  long long before = block_scan(sum, any, warp_sums, &all_need);
   const int total = (int)(all_rows < kSatRows ? all_rows : kSatRows);
   long long taken = 0;  // pages of the admitted requests so far
 #pragma unroll
@@ -272,6 +277,7 @@ page_release_kernel(const __grid_constant__ PageParams p) {
   if (p.expand) wait_for_previous();
   if (!p.finish) let_next_launch();
   const int tid = threadIdx.x, threads = blockDim.x, per = (p.batch + threads - 1) / threads;
+  const bool any = (tid & ~31) * per < p.batch;
   uint32_t status = 0;
 
   int len[kPerThread], cut[kPerThread], gone[kPerThread];
@@ -298,7 +304,7 @@ page_release_kernel(const __grid_constant__ PageParams p) {
     }
   }
   long long all;
-  long long before = block_scan(sum, warp_sums, &all);
+  long long before = block_scan(sum, any, warp_sums, &all);
   const long long room = p.n_pages - free_count;
   long long pushed = 0;
 #pragma unroll
