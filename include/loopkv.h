@@ -498,7 +498,7 @@ typedef struct {
  * (BAD_SLOT).  Slots of one call are distinct (two rows of one slot leave a
  * mixture of both).
  * Errors (nothing launched): LOOPKV_ERR_INVALID_ARG, LOOPKV_ERR_UNSUPPORTED
- * (more than 2^31 blocks of work), LOOPKV_ERR_CUDA. */
+ * (n_rows * n_kv_heads of 2^31 - 128 and more), LOOPKV_ERR_CUDA. */
 loopkv_status loopkv_paged_append(const loopkv_page_pool* pool, const int32_t* h_cells,
                                   int32_t n_cells, int32_t n_rows, const int32_t* d_slots,
                                   const loopkv_rows* k, const loopkv_rows* v, uint32_t* d_status,

@@ -43,7 +43,7 @@ struct PagedAppendParams {
   uint32_t heads;
   int32_t n_slots;      // n_pages * page_size
   int64_t cell_rows;    // token rows of a pool cell
-  PageDiv div;
+  PageDiv div, by_heads;
 };
 
 __device__ __forceinline__ void unpack_bf16(const uint4& x, float (&f)[8]) {
@@ -84,22 +84,30 @@ struct Quantizer {
     scale = range == 0.f ? 0.f : __fdiv_rn(range, 255.f);
     inverse = __frcp_rn(scale);
   }
-  // no step of codes8 can overflow, or underflow where it matters (a quotient near a half)
-  __device__ __forceinline__ bool ordinary() const { return scale > 0x1p-100f && scale < 0x1p100f; }
+  // What codes8 does not cover: scales so small or large that its steps could
+  // underflow or overflow, and those whose last 16 bits are within 8 of 0.
+  __device__ __forceinline__ bool ordinary() const {
+    return scale > 0x1p-100f && scale < 0x1p100f && ((__float_as_uint(scale) + 8u) & 0xffffu) > 16u;
+  }
   __device__ __forceinline__ float zero() const { return low == 0.f ? 0.f : low; }  // a zero minimum is stored as +0
 };
 
-// The codes of 8 values: rne(fl(t / scale)), t = fl(x - low), two values to an
+// The codes of 8 values: rne(fl(t / s)), t = fl(x - low), two values to an
 // instruction.  Quotients on a half step are common (bf16 values are few bits
 // apart), so the rounded quotient itself is needed, and a division takes 10
-// instructions and more per value.  With y the rounded reciprocal of the
-// scale, the rounded quotient is q + y (t - q scale), fused, for any q within one
-// step of it (P. Markstein, "Computation of elementary functions on the IBM RISC
-// System/6000 processor", 1990).  t y is within 1.5 steps, and the same
-// correction once before brings it within one.  rne is the sum with 2^23; the
-// code is then the low byte.
+// instructions and more per value.  With y the rounded reciprocal of s and q0 =
+// fl(t y), q1 = fl(q0 + y (t - q0 s)), fused: one Newton step, whose argument of
+// the last rounding is within 2^-46 of t / s, relatively (y and q0 are off by 2^-24
+// and 2^-23, the residual is rounded by 2^-24 at most, and the products of these
+// remain).  So q1 is fl(t / s) unless t / s is that close to the middle of
+// two floats, and the code can differ only where one of the two is a half step h
+// in [2^e, 2^(e+1)): t = s (h +- 2^(e-24)) (1 + 2^-46).  With s = S 2^a, S of 24
+// bits, t is a multiple of 2^(a+e), so S 2^(e-23) would have to be within 2^(e-20)
+// of an integer: S within 8 of a multiple of 2^(23-e), hence of 2^16, e being 7
+// at most (and for e = -1 no t below s / 2 meets the condition).  Those scales
+// are left to the definition.  rne is the sum with 2^23; the code is then the
+// low byte.
 __device__ __forceinline__ uint2 codes8(const uint4& x, const Quantizer& z) {
-  if (!z.ordinary()) return codes8_exact(x, z.scale, z.low);
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   const uint64_t low = pair(-z.low, -z.low), y = pair(z.inverse, z.inverse), s = pair(-z.scale, -z.scale);
   const uint64_t magic = pair(0x1p23f, 0x1p23f);
@@ -109,11 +117,8 @@ __device__ __forceinline__ uint2 codes8(const uint4& x, const Quantizer& z) {
     uint64_t t = (uint64_t)(w[i] << 16) | (uint64_t)(w[i] & 0xffff0000u) << 32, q, r;
     asm("add.rn.f32x2 %0, %0, %1;" : "+l"(t) : "l"(low));
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(t), "l"(y));
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(q), "l"(s), "l"(t));
-      asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(q) : "l"(r), "l"(y));
-    }
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(q), "l"(s), "l"(t));
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(q) : "l"(r), "l"(y));
     asm("add.rn.f32x2 %0, %0, %1;" : "+l"(q) : "l"(magic));
     c[2 * i] = (uint32_t)q;
     c[2 * i + 1] = (uint32_t)(q >> 32);
@@ -154,7 +159,7 @@ paged_append_kernel(const __grid_constant__ PagedAppendParams p, const __grid_co
   const uint32_t i = blockIdx.x * (uint32_t)(kThreads / LANES) + threadIdx.x / LANES;
   const int part = threadIdx.x % LANES;
   const bool in = i < p.vectors;
-  const uint32_t row = in ? i / p.heads : 0u, head = in ? i - row * p.heads : 0u;
+  const uint32_t row = in ? (uint32_t)p.by_heads.page((int)i) : 0u, head = in ? i - row * p.heads : 0u;
   int slot = in ? p.slots[row] : -1;
   if (slot < -1 || slot >= p.n_slots) {
     if (p.status && part == 0) atomicOr(p.status, LOOPKV_PAGE_BAD_SLOT);
@@ -178,10 +183,20 @@ paged_append_kernel(const __grid_constant__ PagedAppendParams p, const __grid_co
     }
     const Quantizer kz = quantizer<LANES>(extremes(k)), vz = quantizer<LANES>(extremes(v));
     if (slot < 0) return;
+    uint8_t* const kd = p.kp + at * D + part * 8;
+    uint8_t* const vd = p.vp + at * D + part * 8;
+    if (kz.ordinary() && vz.ordinary()) {
 #pragma unroll
-    for (int j = 0; j < kPieces; ++j) {
-      *reinterpret_cast<uint2*>(p.kp + at * D + part * 8 + j * (D / kPieces)) = codes8(k[j], kz);
-      *reinterpret_cast<uint2*>(p.vp + at * D + part * 8 + j * (D / kPieces)) = codes8(v[j], vz);
+      for (int j = 0; j < kPieces; ++j) {
+        *reinterpret_cast<uint2*>(kd + j * (D / kPieces)) = codes8(k[j], kz);
+        *reinterpret_cast<uint2*>(vd + j * (D / kPieces)) = codes8(v[j], vz);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j) {
+        *reinterpret_cast<uint2*>(kd + j * (D / kPieces)) = codes8_exact(k[j], kz.scale, kz.low);
+        *reinterpret_cast<uint2*>(vd + j * (D / kPieces)) = codes8_exact(v[j], vz.scale, vz.low);
+      }
     }
     if (part == 0) p.meta[at] = make_float4(kz.scale, kz.zero(), vz.scale, vz.zero());
   } else {
@@ -243,7 +258,7 @@ extern "C" loopkv_status loopkv_paged_append(const loopkv_page_pool* pool, const
   const int64_t vectors = (int64_t)n_rows * pool->n_kv_heads;
   const bool q8 = pool->format == LOOPKV_PAGE_Q8;
   const int64_t blocks = (vectors * (pool->head_dim / (q8 ? 8 * kPieces : 8)) + kThreads - 1) / kThreads;
-  if (vectors >= (1LL << 32) - kThreads || blocks >= (1LL << 31)) return LOOPKV_ERR_UNSUPPORTED;
+  if (vectors >= (1LL << 31) - kThreads) return LOOPKV_ERR_UNSUPPORTED;
   PagedAppendParams p{};
   p.k = static_cast<const uint16_t*>(k->data);
   p.v = static_cast<const uint16_t*>(v->data);
@@ -263,6 +278,7 @@ extern "C" loopkv_status loopkv_paged_append(const loopkv_page_pool* pool, const
   p.n_slots = pool->n_pages * pool->page_size;
   p.cell_rows = (int64_t)pool->n_pages * pool->n_kv_heads * pool->page_size;
   p.div = PageDiv(pool->page_size);
+  p.by_heads = PageDiv(pool->n_kv_heads);
   const dim3 grid((unsigned)blocks, (unsigned)stored);
   if (pool->head_dim == 64)
     return q8 ? launch_early(paged_append_kernel<64, true>, grid, kThreads, 0, stream, p, cl)
