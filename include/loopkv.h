@@ -440,8 +440,9 @@ typedef enum {
  * reason) are more than the free list has (NO_PAGES).  A page id outside
  * 0 .. n_pages-1 gives slots -1 (BAD_PAGE).  d_free: int32 [n_pages], of which
  * the first *d_free_count are free pages.  d_len_out may be d_len and
- * d_free_count_out may be d_free_count.  d_slots may be NULL (its rows are
- * then only counted), and so may d_newest [batch].
+ * d_free_count_out may be d_free_count (d_len_out equal to d_new is refused).
+ * d_slots may be NULL (its rows are then only counted), and so may d_newest
+ * [batch].
  * Errors (nothing launched): LOOPKV_ERR_INVALID_ARG, LOOPKV_ERR_CUDA. */
 loopkv_status loopkv_page_map(int32_t batch, int32_t page_size, int32_t max_pages, int32_t n_pages,
                               int32_t n_rows, const int32_t* d_len, const int32_t* d_new,
@@ -508,7 +509,7 @@ typedef struct {
   int32_t batch;           /* requests, 1 .. LOOPKV_MAX_PAGED_BATCH */
   int32_t max_pages;       /* table width */
   int32_t q_per_kv;        /* query heads per KV head, 1 .. LOOPKV_MAX_PAGED_GROUP */
-  float sm_scale;          /* <= 0 means 1/sqrt(head_dim) */
+  float sm_scale;          /* <= 0 means 1/sqrt(head_dim); finite, below 2^57 for LOOPKV_PAGE_Q8 */
 } loopkv_paged_desc;
 
 /* Device bytes of workspace that a loopkv_paged_decode of these sizes needs.

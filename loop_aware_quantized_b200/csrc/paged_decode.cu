@@ -5,18 +5,30 @@
 //   s_t = scale <q, k_t>,  m = max s_t,  l = sum exp(s_t - m),
 //   out = sum exp(s_t - m) v_t / l,  lse = m + ln l,
 // one pass over the tokens: every warp keeps its own running (m, l, out) over
-// the 16-token tiles it takes and rescales when its maximum rises; the
-// warps of a CTA are joined through shared memory, the CTAs of a unit through
-// a workspace and a second kernel.  Scores are kept in log2 units.
+// the tiles of 16 or 32 tokens it takes and rescales when its maximum rises by
+// more than weights may grow (kSlack); the warps of a CTA are joined through
+// shared memory, the CTAs of a unit through a workspace and a second kernel.
 //
 // What bounds it: the pages' bytes.  One new token does 4 g D flops on the
 // 4 D bytes (bf16) of a token, g flops a byte where the tensor pipe could
 // take 250.  So every warp keeps its own ring of tiles in shared memory, filled
-// by cp.async two to four tiles ahead (an SM has 100 KB and more in flight, and
+// by cp.async two or three tiles ahead (an SM has 100 KB and more in flight, and
 // one latency of HBM at its share of the bandwidth is 50 KB), without a barrier
 // between warps; keys and values are separate groups, so a tile's keys are
 // replaced while its values are still used.  Rows behind a request's length
-// and rows of bad pages are filled with zeros and not read.
+// and rows of bad pages are filled with zeros and not read.  Direct loads into
+// registers, 12 warps to an SM as here, waited for a tile at a time: 781 us
+// instead of 615 for 32 requests of 16384 tokens, 200 instead of 82 for 67 ragged ones.
+//
+// Measured (bytes of the pages over the time, both kernels): 32 requests of
+// 16384 tokens, 16 heads of 128 in bf16 615 us, 7.0 TB/s; 67 ragged requests of
+// 120000 tokens in 2 cells, 8 heads of 64 with 4 queries in fp16 82 us, 6.0
+// TB/s; at 1 GB pages of 1 token 6.4 TB/s, of 24 tokens 6.2, 8 bits a value 5.7 to
+// 6.1 with 1 and 8 queries and 5.3 with 16, where the conversion of codes (a
+// byte permute per two) takes the issue slots.  Small calls: one request of
+// 4113 tokens, 33.7 MB, 11 us, of which the join's launch and round trips are 3.
+// mma.sync and not tcgen05: a tile of 128 rows would be seven eighths padding and
+// its results a trip to tensor memory away, and the tensor pipe is 5 to 20 % busy.
 //
 // Fragments (lane = 4 r + c).  Scores: m16n8k16 with the queries as A and 8
 // tokens as B (ldmatrix).  The accumulator holds queries r (and r + 8) x
@@ -41,11 +53,12 @@
 // out = sum (p vs) c + sum p vz.
 //
 // Split.  The tiles of all units, in order, are dealt to the workers (one CTA
-// each) in equal contiguous shares, found by every CTA from a prefix sum of
-// the device lengths: ragged lengths, few long requests and many short ones
-// all give every SM the same bytes, and nothing depends on lengths the
-// host may not know.  A worker meets at most one unit that began before it
-// and one that ends behind it: two workspace slots each.
+// each) in equal contiguous shares, a unit's start and end counted as the tiles
+// that they cost, found by every CTA from a prefix sum of the device lengths:
+// ragged lengths, few long requests and many short ones all give every SM the
+// same bytes, and nothing depends on lengths the host may not know.  A worker
+// meets at most one unit that began before it and one that ends behind it: two
+// workspace slots each.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -382,7 +395,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
       const int pos = tile * S::kTok + (lane & (FLAT ? S::kTok - 16 : S::kTok - 1));
       if (tile >= t1 || pos >= np) return {INT_MIN, 0};
       const int j = p.div.page(pos);
-      return {__ldg(entry + j), pos - j * p.div.size};
+      return {entry[j], pos - j * p.div.size};
     };
     auto rows_of = [&](int tile, Next at, uint32_t* row) -> uint32_t {
       const bool good = at.page >= 0 && at.page < p.n_pages;
@@ -424,7 +437,9 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
       const uint32_t at = ring_at + stage * S::kTileBytes;
       copy_rows(at, p.k, row, bits);
       if (Q8 && lane < S::kTok)
-        copy16(at + 2 * S::kRowsBytes + 16 * lane, reinterpret_cast<const uint8_t*>(p.meta + (row + (FLAT ? (uint64_t)(lane & 15) : 0))), (bits >> lane & 1) != 0);
+        copy16(at + 2 * S::kRowsBytes + 16 * lane,
+               reinterpret_cast<const uint8_t*>(p.meta + (row + (FLAT ? (uint64_t)(lane & 15) : 0))),
+               (bits >> lane & 1) != 0);
       copy_commit();
     };
     auto copy_values = [&](int stage, uint32_t row, uint32_t bits) {
@@ -453,10 +468,10 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
           uint2 w = make_uint2(0, 0);
           if (on) {
             if constexpr (!Q8)
-              w = make_uint2(__ldg(reinterpret_cast<const uint32_t*>(src + 16 * i + 2 * c)),
-                             __ldg(reinterpret_cast<const uint32_t*>(src + 16 * i + 8 + 2 * c)));
+              w = make_uint2(*reinterpret_cast<const uint32_t*>(src + 16 * i + 2 * c),
+                             *reinterpret_cast<const uint32_t*>(src + 16 * i + 8 + 2 * c));
             else  // a lane's 4 codes of a 16-byte piece are channels 4 c ..
-              w = __ldg(reinterpret_cast<const uint2*>(src + 16 * i + 4 * c));
+              w = *reinterpret_cast<const uint2*>(src + 16 * i + 4 * c);
           }
           qa[i][MODE == 2 ? half : 0] = w.x;
           qa[i][MODE == 2 ? 2 + half : 1] = w.y;
@@ -679,7 +694,8 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
             dst[16 * j + r] = o[half][j][k];
             dst[16 * j + 8 + r] = o[half][j][2 + k];
           } else {
-            *reinterpret_cast<float2*>(dst + 16 * j + 2 * r) = make_float2(o[half][j][k] * 0x1p69f, o[half][j][2 + k] * 0x1p69f);
+            *reinterpret_cast<float2*>(dst + 16 * j + 2 * r) =
+                make_float2(o[half][j][k] * 0x1p69f, o[half][j][2 + k] * 0x1p69f);
           }
         }
       }
@@ -951,7 +967,9 @@ loopkv_status launch_decode_kernel(PagedDecodeParams p, const Sets& sets, cudaSt
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return LOOPKV_ERR_CUDA;
   const loopkv_status rc = launch_early(kernel, dim3((unsigned)p.workers), kThreads, smem, stream, p, sets);
-  return rc != LOOPKV_OK ? rc : launch_early(paged_join_kernel<D, FMT>, dim3((unsigned)(kJoinOwners * std::min(kJoinSpread, p.rows * (D / 32)))), kJoinThreads, 0, stream, p, sets);
+  if (rc != LOOPKV_OK) return rc;
+  const int blocks = kJoinOwners * std::min(kJoinSpread, p.rows * (D / 32));
+  return launch_early(paged_join_kernel<D, FMT>, dim3((unsigned)blocks), kJoinThreads, 0, stream, p, sets);
 }
 
 template <int D, int FMT, int MODE>
@@ -1073,8 +1091,10 @@ extern "C" loopkv_status loopkv_paged_decode(const loopkv_page_pool* pool, const
   p.scale2 = sm_scale * 1.4426950408889634f;
   const bool q8 = pool->format == LOOPKV_PAGE_Q8;
   p.unit2 = q8 ? p.scale2 * 0x1p69f : p.scale2;
+  if (!std::isfinite(p.unit2)) return LOOPKV_ERR_INVALID_ARG;
   // (finite: the first maximum is -infinity)
-  p.slack = std::min((pool->format == LOOPKV_PAGE_F16 ? Mma<LOOPKV_PAGE_F16>::kSlack : Mma<LOOPKV_PAGE_BF16>::kSlack) / p.unit2, 1e30f);
+  const bool f16 = pool->format == LOOPKV_PAGE_F16;
+  p.slack = std::min((f16 ? Mma<LOOPKV_PAGE_F16>::kSlack : Mma<LOOPKV_PAGE_BF16>::kSlack) / p.unit2, 1e30f);
   p.div = PageDiv(pool->page_size);
   p.by_heads = PageDiv(p.heads);
   p.by_group = PageDiv(p.group);

@@ -420,6 +420,7 @@ extern "C" loopkv_status loopkv_page_map(int32_t batch, int32_t page_size, int32
   for (const void* ptr : ptrs)
     if (ptr == nullptr || !aligned4(ptr)) return LOOPKV_ERR_INVALID_ARG;
   if (!aligned4(d_slots) || !aligned4(d_newest) || !aligned4(d_status)) return LOOPKV_ERR_INVALID_ARG;
+  if (d_len_out == d_new) return LOOPKV_ERR_INVALID_ARG;  // (every block reads the counts)
   PageParams p{};
   p.len = d_len;
   p.count = d_new;

@@ -136,6 +136,15 @@ def test_decode_refuses_arguments(lk):
         assert _decode(lk, pool, current=(1, 1), cur=rows) == INVALID
 
 
+def test_more_refusals(lk):
+    # the new lengths in the place of the counts; a scale that 8-bit scores cannot carry
+    other = ctypes.c_void_p((1 << 20) + 64)
+    p = [FAKE, other, FAKE, FAKE, FAKE, FAKE, other, FAKE]
+    assert _map(lk, ptrs=p) == INVALID
+    pool = _pool(lk, fmt=2, meta=1 << 20)
+    assert _decode(lk, pool, sm_scale=1e20) == INVALID
+
+
 def test_workspace_is_what_decode_asks_for(lk):
     pool = _pool(lk)
     rc, nbytes = lk.loopkv_paged_workspace(pool, lk.loopkv_paged_desc(2, 4, 2, 0.0))
