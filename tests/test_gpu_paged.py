@@ -659,6 +659,69 @@ def test_calls_at_once_on_two_streams(dev):
         assert all((g == want[i]).all() for g in got[i])
 
 
+def test_pages_far_into_a_large_pool(dev):
+    # byte offsets past 2^32: the same tokens in the last pages of a 5 GB pool and in a small one
+    import torch
+    from loop_aware_quantized_b200 import paged_append, paged_decode
+    heads, ps, dim, few = 16, 64, 128, 6
+    n_pages = 5 * (1 << 30) // (heads * ps * dim * 2)
+    lengths, width = ints([130, 64, 100], dev), 3
+    near = np.array([[5, 0, 2], [1, -1, -1], [4, 3, -1]])
+    far = np.where(near >= 0, n_pages - few + near, -1)
+    tables = [ints(near, dev), ints(far, dev)]
+    g = torch.Generator(device=dev).manual_seed(3)
+    k, v = (torch.randn((1, few * ps, heads, dim), generator=g, device=dev).to(torch.bfloat16) for _ in range(2))
+    q = torch.randn((1, 3, 2 * heads, dim), generator=g, device=dev).to(torch.bfloat16)
+    outs = []
+    for pages, first, table in ((few, 0, tables[0]), (n_pages, n_pages - few, tables[1])):
+        kp, vp = (torch.empty((1, pages, heads, ps, dim), dtype=torch.bfloat16, device=dev) for _ in range(2))
+        paged_append([0], k, v, ints(np.arange(few * ps) + first * ps, dev), kp, vp)
+        outs.append(paged_decode([0], q, kp, vp, table, lengths))
+        assert (kp[0, first:].transpose(1, 2).reshape(-1, heads, dim) == k[0]).all()
+        del kp, vp
+    assert width == 3 and (outs[0] == outs[1]).all() and (outs[0] != 0).any()
+
+
+def test_longest_request(dev):
+    # 2^22 tokens: equal scores give the log of their number and the values' mean
+    import math
+    import torch
+    from loop_aware_quantized_b200 import paged_decode
+    n, ps = 1 << 22, 1024
+    kp = torch.zeros((1, n // ps, 1, ps, 64), dtype=torch.bfloat16, device=dev)
+    vp = torch.full_like(kp, 1.5)
+    vp[:, ::2] = -0.5
+    table = ints(np.random.default_rng(0).permutation(n // ps)[None], dev)
+    lse = torch.zeros((1, 1, 3), device=dev)
+    out = paged_decode([0], torch.ones((1, 1, 3, 64), dtype=torch.bfloat16, device=dev), kp, vp, table,
+                       ints([n], dev), lse=lse)
+    # a warp's sum is exact (whole numbers below 2^24), so are the joined ones
+    assert (out == 0.5).all() and (lse - math.log(n)).abs().max() <= 2.0 ** -20 * math.log(n)
+
+
+def test_two_captured_decodes_have_workspaces_of_their_own(dev):
+    # two graphs replayed at once on two streams
+    import torch
+    from loop_aware_quantized_b200 import paged_decode
+    cases = [Case(dev, "bf16", [30000 + i, 10], heads=2, group=4, dim=128, ps=64, seed=30 + i) for i in range(2)]
+    want = [c.run()[0] for c in cases]
+    args = [(c.cells, c.q, c.kp, c.vp, ints(c.table, dev), ints(c.lengths, dev)) for c in cases]
+    outs, graphs, streams = [torch.zeros_like(c.q) for c in cases], [], [torch.cuda.Stream(dev) for _ in cases]
+    torch.cuda.synchronize()
+    for a, out in zip(args, outs):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            paged_decode(*a, out=out)
+            paged_decode(*a, out=out)
+        graphs.append(graph)
+    for _ in range(30):
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    assert all((o == w).all() for o, w in zip(outs, want))
+
+
 def test_refusals_on_the_device(dev):
     import torch
     from loop_aware_quantized_b200 import paged_append, paged_decode
