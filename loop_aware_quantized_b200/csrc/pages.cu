@@ -18,7 +18,7 @@
 // 9.1 us, 8.5 where the outputs lie elsewhere and the grid does it all).  So
 // lengths are updated in place, and a call can be captured and replayed.  What
 // bounds it: the launch and two dependent memory round trips (lengths, then
-// free list or table); 32 requests' step takes 3.9 us, releases of a small batch
+// free list or table); 32 requests' step takes 3.6 us, releases of a small batch
 // 3.5, half a million pages given back 6.7.
 
 #include <cuda_runtime.h>
@@ -42,7 +42,9 @@ constexpr long long kSatRows = 0x7fffffffLL;
 // Exclusive prefix sum over the block's threads; *total gets the sum.  any: the
 // warp has requests (the others only need the barriers; a million rows of 256
 // requests: 8.5 -> 8.2 us).
-__device__ __forceinline__ long long block_scan(long long x, bool any, long long* warp_sums, long long* total) {
+// one: the first warp has all of them, and only it gets a meaningful answer.
+__device__ __forceinline__ long long block_scan(long long x, bool any, bool one, long long* warp_sums,
+                                                long long* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   long long inc = x;
   if (any) {
@@ -51,6 +53,10 @@ __device__ __forceinline__ long long block_scan(long long x, bool any, long long
       const long long y = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += y;
     }
+  }
+  if (one) {
+    *total = __shfl_sync(0xffffffffu, inc, 31);
+    return inc - x;
   }
   __syncthreads();  // the last scan's readers are done
   if (lane == 31) warp_sums[warp] = inc;
@@ -131,7 +137,7 @@ __global__ void __launch_bounds__(kPageThreads) page_map_kernel(const __grid_con
   if (p.expand) wait_for_previous();
   if (!p.finish) let_next_launch();
   const int tid = threadIdx.x, threads = blockDim.x, per = (p.batch + threads - 1) / threads;
-  const bool any = (tid & ~31) * per < p.batch;
+  const bool any = (tid & ~31) * per < p.batch, one = p.batch <= 32;
   uint32_t status = 0;
 
   int len[kPerThread], add[kPerThread];
@@ -150,7 +156,7 @@ __global__ void __launch_bounds__(kPageThreads) page_map_kernel(const __grid_con
     free_count = 0;
   }
   long long all_rows, all_need;
-  long long start = block_scan(rows, any, warp_sums, &all_rows);
+  long long start = block_scan(rows, any, one, warp_sums, &all_rows);
   const long long capacity = (long long)p.max_pages * p.div.size;
   int need[kPerThread];
   long long sum = 0;
@@ -174,8 +180,7 @@ __global__ void __launch_bounds__(kPageThreads) page_map_kernel(const __grid_con
       sum += need[k];
     }
   }
-  long long before = block_scan(sum, any, warp_sums, &all_need);
-  const int total = (int)(all_rows < kSatRows ? all_rows : kSatRows);
+  long long before = block_scan(sum, any, one, warp_sums, &all_need);
   long long taken = 0;  // pages of the admitted requests so far
 #pragma unroll
   for (int k = 0; k < kPerThread; ++k) {
@@ -191,8 +196,9 @@ __global__ void __launch_bounds__(kPageThreads) page_map_kernel(const __grid_con
     sh.b[b] = (int)(free_count - 1 - before);
     before += need[k];
   }
-  if (tid == 0) sh.start[p.batch] = total;
+  if (tid == 0) sh.start[p.batch] = (int)(all_rows < kSatRows ? all_rows : kSatRows);
   __syncthreads();
+  const int total = sh.start[p.batch];
 
   const int lane = tid & 31;
   if (p.expand) {
@@ -277,7 +283,7 @@ page_release_kernel(const __grid_constant__ PageParams p) {
   if (p.expand) wait_for_previous();
   if (!p.finish) let_next_launch();
   const int tid = threadIdx.x, threads = blockDim.x, per = (p.batch + threads - 1) / threads;
-  const bool any = (tid & ~31) * per < p.batch;
+  const bool any = (tid & ~31) * per < p.batch, one = p.batch <= 32;
   uint32_t status = 0;
 
   int len[kPerThread], cut[kPerThread], gone[kPerThread];
@@ -304,7 +310,7 @@ page_release_kernel(const __grid_constant__ PageParams p) {
     }
   }
   long long all;
-  long long before = block_scan(sum, any, warp_sums, &all);
+  long long before = block_scan(sum, any, one, warp_sums, &all);
   const long long room = p.n_pages - free_count;
   long long pushed = 0;
 #pragma unroll
