@@ -197,7 +197,9 @@ loopkv_status launch_early(void (*kernel)(P...), dim3 grid, unsigned threads, si
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? LOOPKV_OK : LOOPKV_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess) return LOOPKV_OK;
+  cudaGetLastError();  // reported here, and by nobody's next check
+  return LOOPKV_ERR_CUDA;
 }
 #endif
 

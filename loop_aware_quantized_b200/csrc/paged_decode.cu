@@ -815,6 +815,7 @@ __device__ __forceinline__ int64_t out_row(const PagedDecodeParams& p, const Set
 template <int D, int FMT>
 __global__ void __launch_bounds__(kJoinThreads)
 paged_join_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_constant__ Sets sets) {
+  require_ieee_subnormals();
   using M = Mma<FMT>;
   constexpr int WARPS = kJoinThreads / 32, LANES = D / 4, CHUNKS = D / 32, GROUPS = kJoinThreads / 8;
   constexpr int PER = (kMaxWorkers + kJoinThreads - 1) / kJoinThreads, FIRST = 4;

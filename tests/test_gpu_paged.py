@@ -118,6 +118,16 @@ def test_page_map_refusals(dev):
     assert check_map(dev, lengths, new, t2, f2, count, ps, 60)[5] & R.BAD_PAGE
 
 
+def test_page_map_without_rows(dev):
+    # a step that brings nothing, and one whose tokens find no row
+    rng = np.random.default_rng(6)
+    lengths = np.array([5, 0, 16, 31])
+    table, free, count = make_tables(rng, lengths, 3, 16, 9)
+    assert check_map(dev, lengths, np.zeros(4, int), table, free, count, 16, 0)[5] == 0
+    assert check_map(dev, lengths, np.array([0, 0, 1, 0]), table, free, count, 16, 0)[5] == R.NO_ROWS
+    check_map(dev, lengths, np.zeros(4, int), table, free, count, 16, 3, in_place=True)
+
+
 def test_page_map_long_prompts(dev):
     # a cluster's rows, more than one chunk per warp, one giant request among small ones
     rng = np.random.default_rng(3)
@@ -534,6 +544,25 @@ def test_decode_reads_strided_vectors(dev):
     c.cur = tuple(fused[:, :, a:a + 2].transpose(0, 1) for a in (4, 6))
     got = c.run(with_cur=True, q=fused[:, :, :4].transpose(0, 1))
     assert (got[0] == want[0]).all() and (got[1] == want[1]).all()
+
+
+def test_decode_reads_broadcast_vectors(dev):
+    # one query row, one current token for every cell and request: strides of zero
+    import torch
+    c = Case(dev, "fp16", [70, 0, 33], heads=2, group=2, dim=64, cells=(0, 0, 0), seed=21)
+    c.q = c.q[:1, :1].expand(3, 3, 4, 64)
+    c.cur = tuple(x[:1, :, :1].expand(3, 3, 2, 64) for x in c.cur)
+    got = c.run(with_cur=True, out=torch.empty((3, 3, 4, 64), dtype=torch.float16, device=dev))
+    c.q, c.cur = c.q.contiguous(), tuple(x.contiguous() for x in c.cur)
+    want = c.check(with_cur=True)
+    assert (got[0] == want[0]).all() and (got[1] == want[1]).all()
+
+
+def test_decode_of_empty_requests_only(dev):
+    for fmt in ("bf16", "q8"):
+        c = Case(dev, fmt, [0] * 70, heads=3, group=5, dim=128, cells=(0, 1), seed=22)
+        c.check()
+        c.check(with_cur=True)
 
 
 def test_decode_on_another_stream(dev):
