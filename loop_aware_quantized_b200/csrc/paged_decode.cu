@@ -272,10 +272,10 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
   constexpr int OS = D + 4;                  // floats of a row in shared memory (banks)
   static_assert(ROWS * OS * 4 <= S::kWarpBytes, "a warp's results take the place of its tiles");
   extern __shared__ __align__(256) uint8_t smem[];
-  float* const sm = reinterpret_cast<float*>(smem + kWarps * S::kWarpBytes);  // [kWarps + 1][kMaxRows] maxima
-  float* const sl = sm + (kWarps + 1) * kMaxRows;                // sums
+  float* const sm = reinterpret_cast<float*>(smem + kWarps * S::kWarpBytes);  // [kWarps + 1][kMaxRows] maxima, factors
+  float* const sl = sm + (kWarps + 1) * kMaxRows;                // sums, one over the joint one
   float* const sz = sl + (kWarps + 1) * kMaxRows;                // [kWarps][kMaxRows] zero-point sums (Q8)
-  int* const prefix = reinterpret_cast<int*>(sz + kWarps * kMaxRows);  // [batch + 1] tiles before a request
+  int* const prefix = reinterpret_cast<int*>(sz + kWarps * kMaxRows);  // [batch + 1] cost before a request
   __shared__ int warp_sums[kWarps];
   __shared__ int64_t out_at[kMaxRows];
   __shared__ const uint16_t* cur_at[kMaxRows];
