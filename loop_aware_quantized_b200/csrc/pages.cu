@@ -32,11 +32,11 @@ namespace loopkv {
 namespace {
 
 constexpr int kPageThreads = 1024;
-constexpr int kFewThreads = 256;  // of a short call of few requests
 constexpr int kPerThread = LOOPKV_MAX_PAGED_BATCH / kPageThreads;  // requests per thread at most
 constexpr int kUnroll = 4;      // rows a lane looks up at a time
 constexpr int kSms = 148;
 constexpr int kShortWork = 4096;  // rows or pages of a one-CTA call
+constexpr int kLongWork = 1 << 18;  // rows or pages that take 512 threads
 constexpr long long kSatRows = 0x7fffffffLL;
 
 // Exclusive prefix sum over the block's threads; *total gets the sum.  any: the
@@ -389,9 +389,14 @@ bool page_args_ok(int32_t batch, int32_t page_size, int32_t max_pages, int32_t n
 }
 
 // work: rows (map) or pages (release) the call may have to expand, at most;
-// threads: of a call of one CTA; in_place: an output takes an input's place.
-loopkv_status launch_pages(void (*kernel)(PageParams), PageParams p, long long work, int threads, bool in_place,
+// in_place: an output takes an input's place; wide: much of the work is sure to
+// be there, in one CTA.  A CTA has as few threads as do (the start of one, its
+// barriers and its idle warps count): 200 requests of which a few end 5.3 us with
+// 1024 and 3.4 with 256, a step of 1024 requests 6.5 with 1024, 7.0 with 256 and 5.8
+// with 512, a million rows 8.3, 8.7 and 8.2.
+loopkv_status launch_pages(void (*kernel)(PageParams), PageParams p, long long work, bool wide, bool in_place,
                            void* stream) {
+  const int threads = wide || p.batch > kPerThread * 512 ? kPageThreads : p.batch > 512 || work > kLongWork ? 512 : 256;
   const size_t smem = sizeof(int) * (3 * (size_t)p.batch + 1);
   if (smem > 40 * 1024 &&  // 48 KB less the static part need no asking
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
@@ -399,12 +404,13 @@ loopkv_status launch_pages(void (*kernel)(PageParams), PageParams p, long long w
   const bool one = work <= kShortWork;
   p.expand = true;
   p.finish = one || !in_place;
-  const long long ctas = one ? 1 : std::min<long long>((work + kPageThreads - 1) / kPageThreads, kSms);
-  const loopkv_status rc = launch_early(kernel, dim3((unsigned)ctas), one ? threads : kPageThreads, smem, stream, p);
+  const long long most = (long long)kSms * kPageThreads / threads;
+  const long long ctas = one ? 1 : std::min<long long>((work + threads - 1) / threads, most);
+  const loopkv_status rc = launch_early(kernel, dim3((unsigned)ctas), threads, smem, stream, p);
   if (rc != LOOPKV_OK || p.finish) return rc;
   p.expand = false;
   p.finish = true;
-  return launch_early(kernel, dim3(1), kPageThreads, smem, stream, p);
+  return launch_early(kernel, dim3(1), threads, smem, stream, p);
 }
 
 }  // namespace
@@ -444,8 +450,8 @@ extern "C" loopkv_status loopkv_page_map(int32_t batch, int32_t page_size, int32
   p.n_pages = n_pages;
   p.n_rows = n_rows;
   p.div = PageDiv(page_size);
-  const int threads = n_rows <= kUnroll * kFewThreads && batch <= kFewThreads ? kFewThreads : kPageThreads;
-  return launch_pages(page_map_kernel, p, n_rows, threads, d_len_out == d_len || d_free_count_out == d_free_count, stream);
+  const bool wide = n_rows > kUnroll * 256 && n_rows <= kShortWork;
+  return launch_pages(page_map_kernel, p, n_rows, wide, d_len_out == d_len || d_free_count_out == d_free_count, stream);
 }
 
 extern "C" loopkv_status loopkv_page_release(int32_t batch, int32_t page_size, int32_t max_pages,
@@ -474,7 +480,7 @@ extern "C" loopkv_status loopkv_page_release(int32_t batch, int32_t page_size, i
   p.n_pages = n_pages;
   p.div = PageDiv(page_size);
   const long long most = std::min<long long>((long long)batch * max_pages, n_pages);
-  // (few of the pages that requests may hold are given back by one call)
-  return launch_pages(page_release_kernel, p, most, batch <= kFewThreads ? kFewThreads : kPageThreads,
+  // (few of the pages that requests may hold are given back by one call: not wide)
+  return launch_pages(page_release_kernel, p, most, false,
                       d_len_out == d_len || d_len_out == d_new_len || d_free_count_out == d_free_count, stream);
 }
