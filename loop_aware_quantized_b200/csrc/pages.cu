@@ -35,7 +35,8 @@ constexpr int kPageThreads = 1024;
 constexpr int kPerThread = LOOPKV_MAX_PAGED_BATCH / kPageThreads;  // requests per thread at most
 constexpr int kUnroll = 4;      // rows a lane looks up at a time
 constexpr int kSms = 148;
-constexpr int kShortWork = 4096;  // rows or pages of a one-CTA call
+constexpr int kShortWork = 256;    // rows or pages of a one-CTA call
+constexpr int kShortRelease = 4096; // pages that requests may hold, of a release in place
 constexpr int kLongWork = 1 << 18;  // rows or pages that take 512 threads
 constexpr long long kSatRows = 0x7fffffffLL;
 
@@ -388,20 +389,23 @@ bool page_args_ok(int32_t batch, int32_t page_size, int32_t max_pages, int32_t n
          (long long)n_pages * page_size < (1LL << 31);
 }
 
-// work: rows (map) or pages (release) the call may have to expand, at most;
-// in_place: an output takes an input's place; wide: much of the work is sure to
-// be there, in one CTA.  A CTA has as few threads as do (the start of one, its
-// barriers and its idle warps count): 200 requests of which a few end 5.3 us with
-// 1024 and 3.4 with 256, a step of 1024 requests 6.5 with 1024, 7.0 with 256 and 5.8
-// with 512, a million rows 8.3, 8.7 and 8.2.
-loopkv_status launch_pages(void (*kernel)(PageParams), PageParams p, long long work, bool wide, bool in_place,
+// work: rows (map) or pages (release) the call may have to expand, at most; one:
+// by one CTA; in_place: an output takes an input's place.  One CTA takes 256
+// rows (700 rows of 30 requests: 4.3 us by one, 4.0 by a grid and a finishing
+// launch, 3.4 by a grid alone; 4000 rows of 200: 6.4, 4.5 and 4.0), a release in
+// place more pages, because few of those that requests may hold are given back
+// by one call (60 requests of 64 pages: 2.5 us by one, 3.0 by two launches).  A
+// CTA has as few threads as do (the start of one, its barriers and its idle
+// warps count): 200 requests of which a few end 5.3 us with 1024 and 3.4 with 256,
+// 1024 rows of 1024 requests by one CTA 6.5 with 1024, 7.0 with 256 and 5.8 with
+// 512, a million rows 8.3, 8.7 and 8.2.
+loopkv_status launch_pages(void (*kernel)(PageParams), PageParams p, long long work, bool one, bool in_place,
                            void* stream) {
-  const int threads = wide || p.batch > kPerThread * 512 ? kPageThreads : p.batch > 512 || work > kLongWork ? 512 : 256;
+  const int threads = p.batch > kPerThread * 512 ? kPageThreads : p.batch > 512 || work > kLongWork ? 512 : 256;
   const size_t smem = sizeof(int) * (3 * (size_t)p.batch + 1);
   if (smem > 40 * 1024 &&  // 48 KB less the static part need no asking
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return LOOPKV_ERR_CUDA;
-  const bool one = work <= kShortWork;
   p.expand = true;
   p.finish = one || !in_place;
   const long long most = (long long)kSms * kPageThreads / threads;
@@ -450,8 +454,7 @@ extern "C" loopkv_status loopkv_page_map(int32_t batch, int32_t page_size, int32
   p.n_pages = n_pages;
   p.n_rows = n_rows;
   p.div = PageDiv(page_size);
-  const bool wide = n_rows > kUnroll * 256 && n_rows <= kShortWork;
-  return launch_pages(page_map_kernel, p, n_rows, wide, d_len_out == d_len || d_free_count_out == d_free_count, stream);
+  return launch_pages(page_map_kernel, p, n_rows, n_rows <= kShortWork, d_len_out == d_len || d_free_count_out == d_free_count, stream);
 }
 
 extern "C" loopkv_status loopkv_page_release(int32_t batch, int32_t page_size, int32_t max_pages,
@@ -480,7 +483,6 @@ extern "C" loopkv_status loopkv_page_release(int32_t batch, int32_t page_size, i
   p.n_pages = n_pages;
   p.div = PageDiv(page_size);
   const long long most = std::min<long long>((long long)batch * max_pages, n_pages);
-  // (few of the pages that requests may hold are given back by one call: not wide)
-  return launch_pages(page_release_kernel, p, most, false,
-                      d_len_out == d_len || d_len_out == d_new_len || d_free_count_out == d_free_count, stream);
+  const bool in_place = d_len_out == d_len || d_len_out == d_new_len || d_free_count_out == d_free_count;
+  return launch_pages(page_release_kernel, p, most, most <= (in_place ? kShortRelease : kShortWork), in_place, stream);
 }

@@ -178,6 +178,20 @@ def test_page_release_refusals(dev):
         assert int(t[4]) == c and int(status) == st and st & R.BAD_LENGTH
 
 
+def test_page_calls_around_a_few_hundred_rows(dev):
+    # one block or many, 256 to 1024 threads, outputs apart or in place
+    for batch, rows in ((30, 255), (30, 256), (30, 257), (513, 256), (513, 600), (512, 1500), (2048, 300),
+                        (2049, 300), (2049, 3000)):
+        rng = np.random.default_rng(batch + rows)
+        lengths = rng.integers(0, 50, batch)
+        new = np.bincount(rng.integers(0, batch, rows), minlength=batch)
+        n_pages = int((-(-(lengths + new) // 8)).sum()) + 2
+        table, free, count = make_tables(rng, lengths, int((lengths + new).max()) // 8 + 1, 8, n_pages)
+        for in_place in (False, True):
+            check_map(dev, lengths, new, table, free, count, 8, rows, in_place)
+            check_map(dev, lengths, new, table, free, count // 2, 8, rows, in_place)
+
+
 # --------------------------------------------------------------- paged_append
 
 def torch_dtype(fmt):
