@@ -8,7 +8,7 @@
 // (Q8: four such pieces of each, a quarter vector apart); a vector's threads sit
 // in one warp, so its minimum and maximum are a few shuffles.  What bounds it:
 // memory.  Each byte is read once and written once; a vector is 128 or 256
-// contiguous bytes on both sides.  36865 rows of 16 heads of 128 in fp16: 94 us, 6.27
+// contiguous bytes on both sides.  36000 rows of 16 heads of 128 in fp16: 94 us, 6.27
 // TB/s.  With a division per value Q8 took more than twice as long as its bytes
 // (2 cells of 16384 rows: 175 us, now 65): see codes8.
 
