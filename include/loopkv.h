@@ -401,7 +401,8 @@ loopkv_status loopkv_vq_encode(const loopkv_vq_desc* desc, const int32_t* h_pos,
  * its kernel ORs LOOPKV_PAGE_* bits where the device data ask for something
  * that cannot be done; what each call does then is written with it.  Nothing
  * outside the given arrays is read or written whatever the device data hold.
- * The arrays of one call must not overlap, except where a call says so. */
+ * The arrays of one call must not overlap, except where a call says so.
+ * Host threads may make paged calls at the same time. */
 typedef enum {
   LOOPKV_PAGE_BF16 = 0,
   LOOPKV_PAGE_F16 = 1,

@@ -184,6 +184,17 @@ struct PageDiv {
 __device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Dynamic shared memory that any call of a kernel may ask for.  The limit belongs to
+// the function and the device, not to the call, so it is the same for every call:
+// one that followed the batch could be lowered by another thread between a call's
+// setting and its launch, which then fails.
+template <typename... P>
+bool allow_shared(void (*kernel)(P...), size_t most) {
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) == cudaSuccess) return true;
+  cudaGetLastError();  // as below
+  return false;
+}
+
 template <typename... P>
 loopkv_status launch_early(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, void* stream,
                            const P&... args) {

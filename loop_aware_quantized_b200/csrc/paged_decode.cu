@@ -962,12 +962,12 @@ template <int D, int FMT, int MODE, bool FLAT>
 loopkv_status launch_decode_kernel(PagedDecodeParams p, const Sets& sets, cudaStream_t stream) {
   using S = Shape<D, FMT, MODE>;
   p.workers = S::kWorkers;
-  const size_t smem = kWarps * S::kWarpBytes + sizeof(float) * (3 * kWarps + 2) * kMaxRows +
-                      sizeof(int) * ((size_t)p.batch + 1);
+  auto smem = [](int batch) {
+    return kWarps * S::kWarpBytes + sizeof(float) * (3 * kWarps + 2) * kMaxRows + sizeof(int) * ((size_t)batch + 1);
+  };
   const auto kernel = paged_decode_kernel<D, FMT, MODE, FLAT>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return LOOPKV_ERR_CUDA;
-  const loopkv_status rc = launch_early(kernel, dim3((unsigned)p.workers), kThreads, smem, stream, p, sets);
+  if (!allow_shared(kernel, smem(LOOPKV_MAX_PAGED_BATCH))) return LOOPKV_ERR_CUDA;
+  const loopkv_status rc = launch_early(kernel, dim3((unsigned)p.workers), kThreads, smem(p.batch), stream, p, sets);
   if (rc != LOOPKV_OK) return rc;
   const int blocks = kJoinOwners * std::min(kJoinSpread, p.rows * (D / 32));
   return launch_early(paged_join_kernel<D, FMT>, dim3((unsigned)blocks), kJoinThreads, 0, stream, p, sets);

@@ -402,10 +402,10 @@ bool page_args_ok(int32_t batch, int32_t page_size, int32_t max_pages, int32_t n
 loopkv_status launch_pages(void (*kernel)(PageParams), PageParams p, long long work, bool one, bool in_place,
                            void* stream) {
   const int threads = p.batch > kPerThread * 512 ? kPageThreads : p.batch > 512 || work > kLongWork ? 512 : 256;
-  const size_t smem = sizeof(int) * (3 * (size_t)p.batch + 1);
-  if (smem > 40 * 1024 &&  // 48 KB less the static part need no asking
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return LOOPKV_ERR_CUDA;
+  auto shared = [](int batch) { return sizeof(int) * (3 * (size_t)batch + 1); };
+  const size_t smem = shared(p.batch);
+  // 48 KB less the static part need no asking
+  if (smem > 40 * 1024 && !allow_shared(kernel, shared(LOOPKV_MAX_PAGED_BATCH))) return LOOPKV_ERR_CUDA;
   p.expand = true;
   p.finish = one || !in_place;
   const long long most = (long long)kSms * kPageThreads / threads;

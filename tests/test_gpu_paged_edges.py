@@ -1,0 +1,89 @@
+"""Paged cells on the GPU at the ends of their ranges."""
+
+import ctypes
+import threading
+
+import numpy as np
+import pytest
+
+from tests.test_gpu_paged import Case, ints
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dev(cuda_device):
+    return cuda_device
+
+
+# ------------------------------------------------------------ two threads
+
+def at_once(calls, times):
+    """Every call of ``calls`` ``times`` times, each in a thread of its own; their nonzero results."""
+    found, gate = [[] for _ in calls], threading.Barrier(len(calls))
+
+    def work(i):
+        gate.wait()
+        found[i] += [rc for rc in (calls[i]() for _ in range(times)) if rc]
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(calls))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    return found
+
+
+def test_decodes_of_two_threads(dev):
+    # a small and the largest batch: the C calls run at once (ctypes drops the interpreter lock)
+    import torch
+    from loop_aware_quantized_b200 import loopkv as lk
+    made = []
+    for i, (batch, fmt) in enumerate(((1, "bf16"), (lk.LOOPKV_MAX_PAGED_BATCH, "bf16"))):
+        c = Case(dev, fmt, [3] * min(batch, 2) + [0] * (batch - 2), heads=1, dim=128, ps=16, seed=i)
+        table, n = ints(c.table, dev), ints(c.lengths, dev)
+        out, stream = torch.zeros_like(c.q), torch.cuda.Stream(dev)
+        pool = lk.loopkv_page_pool(*c.shape[:2], c.ps, 1, 128, lk.LOOPKV_PAGE_BF16, c.kp.data_ptr(), c.vp.data_ptr(), None)
+        desc = lk.loopkv_paged_desc(batch, table.shape[1], 1, 0.0)
+        rc, nbytes = lk.loopkv_paged_workspace(pool, desc)
+        assert rc == 0
+        work = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        rows = lk.loopkv_rows(c.q.data_ptr(), 0, 0 if batch == 1 else 128, 0)
+        cells = np.zeros(1, np.int32)
+        args = (pool, desc, cells.ctypes.data_as(ctypes.c_void_p), None, 1, table.data_ptr(), n.data_ptr(), rows, None, None,
+                out.data_ptr(), None, work.data_ptr(), nbytes, None, stream.cuda_stream)
+        made.append((c, out, args, table, n, work, cells, stream))
+    torch.cuda.synchronize()
+    found = at_once([lambda a=m[2]: lk.loopkv_paged_decode(*a) for m in made], 3000)
+    torch.cuda.synchronize()
+    assert found == [[], []]
+    for c, out, *_ in made:
+        assert (out == c.run()[0]).all()
+
+
+@pytest.mark.parametrize("call", ["map", "release"])
+def test_page_calls_of_two_threads(dev, call):
+    import torch
+    from loop_aware_quantized_b200 import loopkv as lk
+    made = []
+    for batch in (3500, lk.LOOPKV_MAX_PAGED_BATCH):
+        new, table = ints(np.zeros(batch), dev), ints(np.full((batch, 2), -1), dev)
+        free, one = ints(np.arange(16), dev), ints([16], dev)
+        slots, starts = ints(np.zeros(8), dev), ints(np.zeros(batch + 1), dev)
+        n, n_out, one_out = ints(np.zeros(batch), dev), ints(np.full(batch, 5), dev), ints([0], dev)
+        stream = torch.cuda.Stream(dev)
+        p = {k: v.data_ptr() for k, v in dict(n=n, new=new, table=table, free=free, one=one, slots=slots, starts=starts,
+                                             n_out=n_out, one_out=one_out).items()}
+        if call == "map":
+            args = (batch, 16, 2, 16, 8, p["n"], p["new"], p["table"], p["free"], p["one"], p["slots"], p["starts"], None,
+                    p["n_out"], p["one_out"], None, stream.cuda_stream)
+        else:
+            args = (batch, 16, 2, 16, p["n"], p["new"], p["table"], p["free"], p["one"], p["n_out"], p["one_out"], None,
+                    stream.cuda_stream)
+        made.append((args, n_out, one_out, new, table, free, one, slots, starts, n, stream))
+    torch.cuda.synchronize()
+    fn = lk.loopkv_page_map if call == "map" else lk.loopkv_page_release
+    found = at_once([lambda a=m[0]: fn(*a) for m in made], 3000)
+    torch.cuda.synchronize()
+    assert found == [[], []]
+    assert all(not m[1].any() and int(m[2]) == 16 for m in made)
