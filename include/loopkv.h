@@ -461,8 +461,11 @@ loopkv_status loopkv_page_map(int32_t batch, int32_t page_size, int32_t max_page
  * A request is refused (nothing pushed, its length stays) when new < 0, new >
  * len or len > max_pages * page_size (BAD_LENGTH), or when the free list
  * would outgrow n_pages with it (NO_PAGES).  A table entry outside the pool
- * is pushed as -1 (BAD_PAGE; loopkv_page_map gives no slot on it).  d_len_out
- * may be d_len or d_new_len, and d_free_count_out may be d_free_count.
+ * is pushed as -1 (BAD_PAGE; loopkv_page_map gives no slot on it).  A free
+ * count outside 0 .. n_pages counts as a full list here, as an empty one in
+ * loopkv_page_map, and 0 takes its place (BAD_LENGTH): pages may be lost, but
+ * none is given out that a request may hold.  d_len_out may be d_len or
+ * d_new_len, and d_free_count_out may be d_free_count.
  * Errors (nothing launched): LOOPKV_ERR_INVALID_ARG, LOOPKV_ERR_CUDA. */
 loopkv_status loopkv_page_release(int32_t batch, int32_t page_size, int32_t max_pages,
                                   int32_t n_pages, const int32_t* d_len, const int32_t* d_new_len,

@@ -288,10 +288,14 @@ page_release_kernel(const __grid_constant__ PageParams p) {
   uint32_t status = 0;
 
   int len[kPerThread], cut[kPerThread], gone[kPerThread];
-  int free_count = *p.free_count;
-  if (free_count < 0 || free_count > p.n_pages) {
+  int free_count = *p.free_count, room = 0;
+  if (free_count >= 0 && free_count <= p.n_pages) {
+    room = p.n_pages - free_count;
+  } else {
+    // Nothing is pushed, and the count that is stored offers no page: where the
+    // free pages are is not known, and requests may hold any of the list's.
     status |= LOOPKV_PAGE_BAD_LENGTH;
-    free_count = p.n_pages;  // nothing can be pushed
+    free_count = 0;
   }
   const long long capacity = (long long)p.max_pages * p.div.size;
   long long sum = 0;
@@ -312,7 +316,6 @@ page_release_kernel(const __grid_constant__ PageParams p) {
   }
   long long all;
   long long before = block_scan(sum, any, one, warp_sums, &all);
-  const long long room = p.n_pages - free_count;
   long long pushed = 0;
 #pragma unroll
   for (int k = 0; k < kPerThread; ++k) {

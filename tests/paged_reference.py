@@ -56,10 +56,9 @@ def page_release(lengths, new, table, free, count, ps):
     free = free.copy()
     batch, width = table.shape
     out = lengths.astype(np.int64).copy()
-    status = 0
+    status, room, asked = 0, free.size - count, 0
     if not 0 <= count <= free.size:
-        status, count = BAD_LENGTH, free.size
-    room, asked = free.size - count, 0
+        status, count, room = BAD_LENGTH, 0, 0      # nothing is pushed, no page is offered
     for b in range(batch):
         n, a = int(lengths[b]), int(new[b])
         if a < 0 or a > n or n > width * ps:

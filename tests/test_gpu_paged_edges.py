@@ -6,7 +6,8 @@ import threading
 import numpy as np
 import pytest
 
-from tests.test_gpu_paged import Case, ints
+from tests import paged_reference as R
+from tests.test_gpu_paged import Case, check_map, host, ints, make_tables
 
 pytestmark = pytest.mark.gpu
 
@@ -87,3 +88,29 @@ def test_page_calls_of_two_threads(dev, call):
     torch.cuda.synchronize()
     assert found == [[], []]
     assert all(not m[1].any() and int(m[2]) == 16 for m in made)
+
+
+# ------------------------------------------------------- damaged bookkeeping
+
+@pytest.mark.parametrize("bad", [-1, -2 ** 31, 1, 2 ** 31 - 1])
+@pytest.mark.parametrize("batch,width", [(3, 4), (70, 5), (900, 9)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_release_with_a_count_out_of_range_hands_out_nothing(dev, bad, batch, width, in_place):
+    # no page is pushed, and the count that is stored holds no page that a request still has
+    from loop_aware_quantized_b200 import page_release
+    rng = np.random.default_rng(batch)
+    ps, n_pages = 8, batch * width
+    if bad == 1:
+        bad = n_pages + 1
+    lengths = rng.integers(1, width * ps + 1, batch)
+    table, free, _ = make_tables(rng, lengths, width, ps, n_pages)
+    new = np.where(rng.random(batch) < 0.7, 0, lengths - 1)
+    t = [ints(x, dev) for x in (lengths, new, table, free, [bad])]
+    status = ints([0], dev)
+    lo, co = (t[0], t[4]) if in_place else (ints(np.full(batch, 99), dev), ints([99], dev))
+    page_release(*t, ps, lengths_out=None if in_place else lo, free_count_out=None if in_place else co, status=status)
+    pushes = -(-lengths // ps) > -(-new // ps)
+    assert np.array_equal(host(t[3]), free) and int(co) == 0
+    assert np.array_equal(host(lo), np.where(pushes, lengths, new))
+    assert int(status) == R.BAD_LENGTH | R.NO_PAGES
+    check_map(dev, host(lo), np.full(batch, ps), host(t[2]), free, int(co), ps, batch * ps)
