@@ -65,7 +65,6 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <climits>
 #include <cmath>
 #include <cstdint>
 
@@ -389,17 +388,17 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
     // token to be read.
     const int32_t* const entry = p.table + (int64_t)b * p.max_pages;
     struct Next {
-      int page, off;
+      int page, off;  // off < 0: no token of the pages
     };
     auto page_of = [&](int tile) -> Next {
       const int pos = tile * S::kTok + (lane & (FLAT ? S::kTok - 16 : S::kTok - 1));
-      if (tile >= t1 || pos >= np) return {INT_MIN, 0};
+      if (tile >= t1 || pos >= np) return {-1, -1};
       const int j = p.div.page(pos);
       return {entry[j], pos - j * p.div.size};
     };
     auto rows_of = [&](int tile, Next at, uint32_t* row) -> uint32_t {
       const bool good = at.page >= 0 && at.page < p.n_pages;
-      if (!good && at.page != INT_MIN) status |= LOOPKV_PAGE_BAD_PAGE;
+      if (!good && at.off >= 0) status |= LOOPKV_PAGE_BAD_PAGE;
       *row = good ? cell_row + (uint32_t)at.page * page_rows + (uint32_t)at.off : 0u;
       const uint32_t found = __ballot_sync(0xffffffffu, good) & S::kAll;
       const int left = np - tile * S::kTok;

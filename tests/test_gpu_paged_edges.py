@@ -114,3 +114,13 @@ def test_release_with_a_count_out_of_range_hands_out_nothing(dev, bad, batch, wi
     assert np.array_equal(host(lo), np.where(pushes, lengths, new))
     assert int(status) == R.BAD_LENGTH | R.NO_PAGES
     check_map(dev, host(lo), np.full(batch, ps), host(t[2]), free, int(co), ps, batch * ps)
+
+
+def test_decode_flags_every_page_id_outside_the_pool(dev):
+    for fmt in ("bf16", "q8"):
+        for ps in (16, 24):
+            c = Case(dev, fmt, [100, 64, 20], heads=2, group=2, ps=ps, seed=40)
+            for bad in (-2 ** 31, -2 ** 31 + 1, -1, c.shape[1], 2 ** 31 - 1):
+                t = c.table.copy()
+                t[0, 1] = bad
+                c.check(table=t, status=R.BAD_PAGE)
