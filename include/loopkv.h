@@ -538,8 +538,12 @@ loopkv_status loopkv_paged_workspace(const loopkv_page_pool* pool, const loopkv_
  * lse -infinity.  Lengths below 0 or above max_pages * page_size count as 0
  * (BAD_LENGTH); tokens on a page outside the pool are left out (BAD_PAGE).
  * What pages hold behind a request's length has no influence.  Softmax weights
- * are kept to about 16 bits (bf16 pairs) where they meet the values, sums are
- * fp32; the order of all sums is fixed by the sizes and lengths.
+ * are kept as a pair of 16-bit floats where they meet the values: to 2^-16 of
+ * themselves, or to 2^-133 (bf16) and 2^-38 (fp16) of the largest weight if
+ * that is more.  An infinite value gives infinity where its weight is 2^-126
+ * (fp16: 2^-38) of the largest or more, else possibly NaN.  Sums are fp32 of weights up to 2^8: 16-bit values
+ * above 2^98 may overflow them.  The order of all sums is fixed by the sizes
+ * and lengths.
  * Errors (nothing launched): LOOPKV_ERR_INVALID_ARG (null or misaligned
  * pointers, sizes, a workspace below loopkv_paged_workspace's bytes),
  * LOOPKV_ERR_CUDA. */

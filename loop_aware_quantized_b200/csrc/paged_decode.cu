@@ -39,9 +39,12 @@
 // output: with up to 4 query rows the rows r + 4 of A repeat the queries and
 // their lanes take the lo part (no instruction more), otherwise a second
 // product adds it.
-// hi is cut towards zero and lo kept above zero (kTiny, far below any weight's
-// rounding), so that an infinite value stays infinite and is no NaN.
-// fp16 weights are scaled by 2^14 so that small ones keep their bits.
+// hi is cut towards zero, and lo is the type's smallest step at least where hi is
+// not zero (weight_lo), so that an infinite value times a weight stays infinite
+// (0 times infinity is NaN) while a weight of zero adds nothing.  fp16 weights are
+// scaled by 2^14 so that small ones keep their bits.  A weight is so kept to 2^-16
+// of itself or, if that is more, to the smallest step relative to the largest
+// weight of the warp: 2^-133 in bf16, 2^-24 / 2^14 = 2^-38 in fp16.
 //
 // Cells that share.  Listed cells that read the same pool cell are one unit
 // with all their query rows (Sets), so their pages are read once.
@@ -144,7 +147,13 @@ struct Mma<LOOPKV_PAGE_BF16> {
   static __device__ __forceinline__ uint32_t pack_down(float x, float y) {  // towards zero
     return __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
   }
-  static constexpr float kTiny = 0x1p-100f;
+  // the lo part of weights beside their hi part
+  static __device__ __forceinline__ uint32_t weight_lo(uint32_t hi, float lo0, float lo1) {
+    uint32_t least, w;
+    asm("min.bf16x2 %0, %1, %2;" : "=r"(least) : "r"(hi), "r"(0x00010001u));
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(w) : "r"(pack(lo0, lo1)), "r"(least));
+    return w;
+  }
   static __device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
   static __device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
   static constexpr float kShift = 0.f;
@@ -168,7 +177,12 @@ struct Mma<LOOPKV_PAGE_F16> {
     asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(y), "f"(x));
     return w;
   }
-  static constexpr float kTiny = 0x1p-24f;
+  static __device__ __forceinline__ uint32_t weight_lo(uint32_t hi, float lo0, float lo1) {
+    uint32_t least, w;
+    asm("min.f16x2 %0, %1, %2;" : "=r"(least) : "r"(hi), "r"(0x00010001u));
+    asm("max.f16x2 %0, %1, %2;" : "=r"(w) : "r"(pack(lo0, lo1)), "r"(least));
+    return w;
+  }
   static __device__ __forceinline__ float lo(uint32_t w) {
     return __half2float(__ushort_as_half((unsigned short)(w & 0xffffu)));
   }
@@ -621,12 +635,8 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_co
 #pragma unroll
         for (int g = 0; g < S::kGroups; ++g) {
           ph[half][g] = M::pack_down(e[g][0], e[g][1]);
-          float lo0 = e[g][0] - M::lo(ph[half][g]), lo1 = e[g][1] - M::hi(ph[half][g]);
-          if constexpr (!Q8) {  // codes are finite
-            lo0 = fmaxf(lo0, M::kTiny);
-            lo1 = fmaxf(lo1, M::kTiny);
-          }
-          pl[half][g] = M::pack(lo0, lo1);
+          const float lo0 = e[g][0] - M::lo(ph[half][g]), lo1 = e[g][1] - M::hi(ph[half][g]);
+          pl[half][g] = Q8 ? M::pack(lo0, lo1) : M::weight_lo(ph[half][g], lo0, lo1);  // (codes are finite)
           if (MODE == 0 && r >= 4) ph[half][g] = pl[half][g];
         }
       }

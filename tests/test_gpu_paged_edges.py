@@ -124,3 +124,52 @@ def test_decode_flags_every_page_id_outside_the_pool(dev):
                 t = c.table.copy()
                 t[0, 1] = bad
                 c.check(table=t, status=R.BAD_PAGE)
+
+
+# ------------------------------------------------------------------- weights
+
+def dominated(dev, fmt, gap, value, n=512, batch=888, group=1):
+    """Requests whose first token, of value 0, lies ``gap`` nats above the others, of value ``value``."""
+    c = Case(dev, fmt, [n] * batch, heads=1, group=group, dim=64, ps=16, seed=50, width=n // 16)
+    c.q.zero_()
+    c.q[..., 0] = 1
+    c.kp.zero_()
+    c.vp.fill_(value)
+    c.kp[0, c.table[:, 0], 0, 0, 0] = gap
+    c.vp[0, c.table[:, 0], 0, 0] = 0
+    return c
+
+
+@pytest.mark.parametrize("group", [1, 8, 16])
+@pytest.mark.parametrize("fmt,gap,value", [
+    ("bf16", 300, 2.0 ** 120), ("bf16", 300, -2.0 ** 120), ("bf16", 75, 2.0 ** 100), ("bf16", 20, 2.0 ** 100),
+    ("bf16", 300, 1.0), ("fp16", 300, 60000.0), ("fp16", 40, 60000.0), ("fp16", 40, -60000.0), ("fp16", 5, 60000.0)])
+def test_decode_adds_nothing_for_weights_of_nothing(dev, fmt, gap, value, group):
+    dominated(dev, fmt, gap, value, batch=888 if group == 1 else 50, group=group).check(sm_scale=1.0)
+
+
+@pytest.mark.parametrize("gap", [14.0, 18.0, 22.0, 26.0])
+def test_decode_fp16_weights_near_their_smallest_step(dev, gap):
+    # a weight is kept to 2^-38 of the largest where that is more than 2^-16 of itself
+    n, value = 512, 60000.0
+    c = dominated(dev, "fp16", gap, value, n)
+    out, lse, status = c.run(sm_scale=1.0)
+    want = (n - 1) * np.exp(-gap) * value / (1 + (n - 1) * np.exp(-gap))
+    tol, _ = R.bounds(np.full((1, 1), want), np.full((1, 1), want), np.full(1, gap), n, 2.0 ** -11)
+    assert status == 0 and (np.abs(host(out).astype(np.float64) - want) <= tol + n * value * 2.0 ** -38).all()
+
+
+@pytest.mark.parametrize("group", [1, 8, 16])
+@pytest.mark.parametrize("fmt,gaps", [("bf16", (0, 1, 20, 80)), ("fp16", (0, 1, 10, 20, 25))])
+def test_decode_keeps_infinite_values_infinite(dev, fmt, gaps, group):
+    # at the largest weight, at middle ones, and at those next to the smallest that are kept
+    for gap in gaps:
+        for sign in (1, -1):
+            c = dominated(dev, fmt, gap, 1.0, n=64, batch=5, group=group)
+            c.vp[0, c.table[2, 1], 0, 3, 7] = sign * float("inf")
+            c.vp[0, c.table[3, 0], 0, 0, 9] = sign * float("inf")
+            out, _, _ = c.run(sm_scale=1.0)
+            o = host(out)[0]
+            assert (o[2, :, 7] == sign * np.inf).all() and (o[3, :, 9] == sign * np.inf).all()
+            o[2, :, 7] = o[3, :, 9] = 0
+            assert np.isfinite(o).all()
