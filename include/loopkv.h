@@ -388,7 +388,10 @@ loopkv_status loopkv_vq_encode(const loopkv_vq_desc* desc, const int32_t* h_pos,
  * as +0), code = rne(fl(fl(x - min) / scale)) clamped to 0..255, scale 0
  * giving codes 0: the quantizer of the 4-bit cells with 255 steps, grouped
  * per token for keys too, since pages take tokens one at a time and in any
- * order.  Inputs of a Q8 append are finite.
+ * order.  A vector that 8 bits cannot hold - one with NaN or an infinity, or of
+ * a range beyond fp32 - gets codes 0 and a scale that is not finite, so that
+ * its token decodes as NaN, and LOOPKV_PAGE_BAD_VALUE; so is a value vector
+ * flagged whose scale is 2^56 or more, which decode cannot weigh.
  * Tables.  d_table: int32 [batch][max_pages]; token t of request b is in
  * page d_table[b][t / page_size] at offset t % page_size.  Entries behind a
  * request's last page mean nothing and are never read.  slot = page *
@@ -420,6 +423,7 @@ typedef enum {
 #define LOOPKV_PAGE_NO_PAGES 8u   /* the free list is too short (or too full to push to) */
 #define LOOPKV_PAGE_BAD_PAGE 16u  /* a table or free-list entry outside the pool */
 #define LOOPKV_PAGE_BAD_SLOT 32u  /* a slot outside the pool */
+#define LOOPKV_PAGE_BAD_VALUE 64u /* a vector that Q8 pages cannot hold */
 
 /* Room for new tokens: block tables and slot map from request lengths.  For
  * request b < batch, holding d_len[b] tokens and bringing d_new[b]:
@@ -500,8 +504,8 @@ typedef struct {
  * stores nothing and is skipped), row r < n_rows and head h, vectors (i, r, h)
  * of k and v go to slot d_slots[r] of cell c, as they are or quantized (Q8).
  * Rows with slot -1 are skipped, slots below -1 or outside the pool too
- * (BAD_SLOT).  Slots of one call are distinct (two rows of one slot leave a
- * mixture of both).
+ * (BAD_SLOT).  Q8 flags vectors that it cannot hold (BAD_VALUE).  Slots of one
+ * call are distinct (two rows of one slot leave a mixture of both).
  * Errors (nothing launched): LOOPKV_ERR_INVALID_ARG, LOOPKV_ERR_UNSUPPORTED
  * (n_rows * n_kv_heads of 2^31 - 128 and more), LOOPKV_ERR_CUDA. */
 loopkv_status loopkv_paged_append(const loopkv_page_pool* pool, const int32_t* h_cells,
@@ -541,9 +545,9 @@ loopkv_status loopkv_paged_workspace(const loopkv_page_pool* pool, const loopkv_
  * are kept as a pair of 16-bit floats where they meet the values: to 2^-16 of
  * themselves, or to 2^-133 (bf16) and 2^-38 (fp16) of the largest weight if
  * that is more.  An infinite value gives infinity where its weight is 2^-126
- * (fp16: 2^-38) of the largest or more, else possibly NaN.  Sums are fp32 of weights up to 2^8: 16-bit values
- * above 2^98 may overflow them.  The order of all sums is fixed by the sizes
- * and lengths.
+ * (fp16: 2^-38) of the largest or more, else possibly NaN.  Sums are fp32 of
+ * weights up to 2^8: 16-bit values above 2^98 may overflow them.  The order of
+ * all sums is fixed by the sizes and lengths.
  * Errors (nothing launched): LOOPKV_ERR_INVALID_ARG (null or misaligned
  * pointers, sizes, a workspace below loopkv_paged_workspace's bytes),
  * LOOPKV_ERR_CUDA. */

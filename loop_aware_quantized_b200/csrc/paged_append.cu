@@ -59,7 +59,8 @@ __device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, ui
   return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
-// By the definition, one value after another.
+// By the definition, one value after another.  Where the scale is not finite, the
+// quotients are 0 or NaN, which converts to 0.
 __device__ __noinline__ uint2 codes8_exact(uint4 x, float scale, float low) {
   float f[8];
   unpack_bf16(x, f);
@@ -126,7 +127,8 @@ __device__ __forceinline__ uint2 codes8(const uint4& x, const Quantizer& z) {
   return make_uint2(pack4(c[0], c[1], c[2], c[3]), pack4(c[4], c[5], c[6], c[7]));
 }
 
-// The smallest and the negated largest of a thread's bf16 values, as a pair.
+// The smallest and the negated largest of a thread's bf16 values, as a pair; NaN
+// if there is one, so that it reaches scale and zero point.
 __device__ __forceinline__ __nv_bfloat162 extremes(const uint4 (&x)[kPieces]) {
   __nv_bfloat162 mn = *reinterpret_cast<const __nv_bfloat162*>(&x[0].x), mx = mn;
 #pragma unroll
@@ -135,18 +137,18 @@ __device__ __forceinline__ __nv_bfloat162 extremes(const uint4 (&x)[kPieces]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(&w[i]);
-      mn = __hmin2(mn, v);
-      mx = __hmax2(mx, v);
+      mn = __hmin2_nan(mn, v);
+      mx = __hmax2_nan(mx, v);
     }
   }
-  return __halves2bfloat162(__hmin(__low2bfloat16(mn), __high2bfloat16(mn)),
-                            __hneg(__hmax(__low2bfloat16(mx), __high2bfloat16(mx))));
+  return __halves2bfloat162(__hmin_nan(__low2bfloat16(mn), __high2bfloat16(mn)),
+                            __hneg(__hmax_nan(__low2bfloat16(mx), __high2bfloat16(mx))));
 }
 
 template <int LANES>
 __device__ __forceinline__ Quantizer quantizer(__nv_bfloat162 e) {
 #pragma unroll
-  for (int o = LANES / 2; o > 0; o >>= 1) e = __hmin2(e, __shfl_xor_sync(0xffffffffu, e, o));
+  for (int o = LANES / 2; o > 0; o >>= 1) e = __hmin2_nan(e, __shfl_xor_sync(0xffffffffu, e, o));
   return Quantizer(__low2float(e), -__high2float(e));
 }
 
@@ -198,7 +200,11 @@ paged_append_kernel(const __grid_constant__ PagedAppendParams p, const __grid_co
         *reinterpret_cast<uint2*>(vd + j * (D / kPieces)) = codes8_exact(v[j], vz.scale, vz.low);
       }
     }
-    if (part == 0) p.meta[at] = make_float4(kz.scale, kz.zero(), vz.scale, vz.zero());
+    if (part == 0) {
+      p.meta[at] = make_float4(kz.scale, kz.zero(), vz.scale, vz.zero());
+      // (also for NaN; decode carries value scales times 2^64 and weights up to 2^8 in bf16)
+      if (p.status && !(kz.scale < INFINITY && vz.scale < 0x1p56f)) atomicOr(p.status, LOOPKV_PAGE_BAD_VALUE);
+    }
   } else {
     if (slot < 0) return;
     const uint4 k = *reinterpret_cast<const uint4*>(ks), v = *reinterpret_cast<const uint4*>(vs);

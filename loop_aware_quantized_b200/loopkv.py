@@ -26,7 +26,7 @@ LOOPKV_MAX_PAGED_BATCH = 4096
 LOOPKV_MAX_PAGED_TOKENS = 1 << 22
 LOOPKV_MAX_PAGED_GROUP = 16
 LOOPKV_PAGE_BAD_LENGTH, LOOPKV_PAGE_NO_TABLE, LOOPKV_PAGE_NO_ROWS = 1, 2, 4
-LOOPKV_PAGE_NO_PAGES, LOOPKV_PAGE_BAD_PAGE, LOOPKV_PAGE_BAD_SLOT = 8, 16, 32
+LOOPKV_PAGE_NO_PAGES, LOOPKV_PAGE_BAD_PAGE, LOOPKV_PAGE_BAD_SLOT, LOOPKV_PAGE_BAD_VALUE = 8, 16, 32, 64
 
 STATUS = {
     0: "LOOPKV_OK",

@@ -7,7 +7,7 @@ import numpy as np
 import pytest
 
 from tests import paged_reference as R
-from tests.test_gpu_paged import Case, check_map, host, ints, make_tables
+from tests.test_gpu_paged import Case, check_map, empty_pool, host, ints, make_tables
 
 pytestmark = pytest.mark.gpu
 
@@ -173,3 +173,58 @@ def test_decode_keeps_infinite_values_infinite(dev, fmt, gaps, group):
             assert (o[2, :, 7] == sign * np.inf).all() and (o[3, :, 9] == sign * np.inf).all()
             o[2, :, 7] = o[3, :, 9] = 0
             assert np.isfinite(o).all()
+
+
+# -------------------------------------------------- 8-bit pages, any input
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_q8_append_keeps_the_trace_of_what_it_cannot_hold(dev, dim):
+    # NaN, infinities and ranges beyond fp32: flagged, and the token decodes as NaN; its neighbours
+    # are as they would be without it
+    import torch
+    from loop_aware_quantized_b200 import loopkv as lk, paged_append, paged_decode
+    heads, ps, rows = 2, 8, 8
+    g = torch.Generator(device=dev).manual_seed(dim)
+    k, v, q = (torch.randn((1, rows, heads, dim), generator=g, device=dev).to(torch.bfloat16) for _ in range(3))
+    top = torch.finfo(torch.bfloat16).max
+    for part in (0, 1):
+        for at in (0, dim // 2 + 3, dim - 1):
+            for bad in (float("nan"), float("inf"), -float("inf"), "range"):
+                kv = [k.clone(), v.clone()]
+                if bad == "range":
+                    kv[part][0, 5, 1, 1 - min(at, 1)], kv[part][0, 5, 1, at] = -top, top
+                else:
+                    kv[part][0, 5, 1, at] = bad
+                kp, vp, meta = empty_pool(dev, "q8", (1, 1, heads, ps, dim))
+                meta.zero_()
+                status = ints([0], dev)
+                paged_append([0], *kv, ints(np.arange(rows), dev), kp, vp, meta=meta, status=status)
+                assert int(status) == lk.LOOPKV_PAGE_BAD_VALUE
+                pages = host((kp, vp)[part])[0, 0]
+                code, scale, zero = R.quantize(host((k, v)[part][0]))
+                others = np.ones((heads, ps), bool)
+                others[1, 5] = False
+                assert np.array_equal(pages[others], code.transpose(1, 0, 2)[others]) and not pages[1, 5].any()
+                out = host(paged_decode([0], q[:, :1], kp, vp, ints([[0]], dev), ints([rows], dev), meta=meta))
+                assert np.isnan(out[0, 0, 1]).all() and np.isfinite(out[0, 0, 0]).all()
+
+
+def test_q8_append_flags_value_ranges_that_decode_cannot_weigh(dev):
+    # scales of values from 2^56 on; keys may have them
+    import torch
+    from loop_aware_quantized_b200 import loopkv as lk, paged_append, paged_decode
+    x = torch.zeros((1, 3, 1, 64), dtype=torch.bfloat16, device=dev)
+    q = torch.zeros((1, 1, 1, 64), dtype=torch.bfloat16, device=dev)
+    for power, want in ((55, 0), (56, lk.LOOPKV_PAGE_BAD_VALUE)):
+        big = x.clone()
+        big[0, 1, 0, 5] = 255 * 2.0 ** power
+        for kv, flag in (((x, big), want), ((big, x), 0)):
+            kp, vp, meta = empty_pool(dev, "q8", (1, 1, 1, 4, 64))
+            status = ints([0], dev)
+            paged_append([0], *kv, ints([0, 1, 2], dev), kp, vp, meta=meta, status=status)
+            assert int(status) == flag
+            if flag == 0:  # equal scores: the mean of the three
+                out = host(paged_decode([0], q, kp, vp, ints([[0]], dev), ints([3], dev), meta=meta))[0, 0, 0]
+                ref = R.decode([0], host(q), host(kp), host(vp), host(meta), np.array([[0]]), [3], 4)
+                tol, _ = R.bounds(ref[0], ref[2], ref[3], 3, 2.0 ** -8)
+                assert (np.abs(out - ref[0][0, 0, 0]) <= tol[0, 0, 0]).all()
