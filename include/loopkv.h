@@ -546,8 +546,11 @@ loopkv_status loopkv_paged_workspace(const loopkv_page_pool* pool, const loopkv_
  * themselves, or to 2^-133 (bf16) and 2^-38 (fp16) of the largest weight if
  * that is more.  An infinite value gives infinity where its weight is 2^-126
  * (fp16: 2^-38) of the largest or more, else possibly NaN.  Sums are fp32 of
- * weights up to 2^8: 16-bit values above 2^98 may overflow them.  The order of
- * all sums is fixed by the sizes and lengths.
+ * weights up to 2^8: 16-bit values above 2^98 may overflow them.  For Q8,
+ * queries lie below 2^64 in magnitude (they meet the codes times 2^64 in bf16;
+ * larger ones give NaN or infinity) and scales of values below 2^56
+ * (LOOPKV_PAGE_BAD_VALUE).  The order of all sums is fixed by the sizes and
+ * lengths.
  * Errors (nothing launched): LOOPKV_ERR_INVALID_ARG (null or misaligned
  * pointers, sizes, a workspace below loopkv_paged_workspace's bytes),
  * LOOPKV_ERR_CUDA. */

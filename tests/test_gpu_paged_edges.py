@@ -228,3 +228,12 @@ def test_q8_append_flags_value_ranges_that_decode_cannot_weigh(dev):
                 ref = R.decode([0], host(q), host(kp), host(vp), host(meta), np.array([[0]]), [3], 4)
                 tol, _ = R.bounds(ref[0], ref[2], ref[3], 3, 2.0 ** -8)
                 assert (np.abs(out - ref[0][0, 0, 0]) <= tol[0, 0, 0]).all()
+
+
+def test_q8_decode_reads_the_largest_queries(dev):
+    # queries just below 2^64, key scales that bring their scores down
+    c = Case(dev, "q8", [40, 7], heads=1, group=2, dim=64, seed=60)
+    c.q.fill_(2.0 ** 64 * (1 - 2.0 ** -8))
+    c.meta[..., 0] *= 2.0 ** -64
+    c.meta[..., 1] = 0
+    c.check()
