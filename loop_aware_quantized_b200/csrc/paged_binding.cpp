@@ -312,6 +312,7 @@ PyObject* paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
       PyErr_Clear();
       return status(kNotPlain);
     }
+    if (scale > 0 && static_cast<float>(scale) == 0.f) return status(kNotPlain);
     const loopkv_paged_desc desc{(int32_t)batch, (int32_t)width, (int32_t)(q.heads / pool.c.n_kv_heads), (float)scale};
     size_t bytes = 0;
     loopkv_status rc = workspace_fn(&pool.c, &desc, &bytes);

@@ -309,6 +309,8 @@ def paged_decode(cells, q, k_pages, v_pages, table, lengths, meta=None, cur_k=No
             flags = b"\1" * n_cells
     group = q_heads // heads
     desc = _lk.loopkv_paged_desc(batch, width, group, float(sm_scale))
+    if sm_scale > 0 and desc.sm_scale == 0:  # (0 would mean 1 / sqrt(head dim))
+        raise _invalid(where, "sm_scale %r is 0 in fp32" % sm_scale)
     d_status = None if status is None else _ints(status, where, "status", index, (1,))
     d_out = None if out is None else _full(out, where, "out", dtype, index, q.shape)
     d_lse = None if lse is None else _full(lse, where, "lse", _F32, index, q.shape[:3])

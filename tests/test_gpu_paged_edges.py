@@ -237,3 +237,20 @@ def test_q8_decode_reads_the_largest_queries(dev):
     c.meta[..., 0] *= 2.0 ** -64
     c.meta[..., 1] = 0
     c.check()
+
+
+# ----------------------------------------------------- arguments, both ways
+
+def test_positive_scales_that_fp32_loses_are_refused(dev):
+    # (a scale of 0 means 1 / sqrt(head dim))
+    import torch
+    from loop_aware_quantized_b200 import paged_decode
+    from loop_aware_quantized_b200.loopkv import LoopKVError
+    c = Case(dev, "bf16", [10, 20], heads=2, group=2, dim=64, seed=61)
+    t, n = ints(c.table, dev), ints(c.lengths, dev)
+    for stream in (None, torch.cuda.current_stream()):
+        for scale in (1e-50, 2.0 ** -150, 1e300):
+            with pytest.raises(LoopKVError) as e:
+                paged_decode([0], c.q, c.kp, c.vp, t, n, sm_scale=scale, stream=stream)
+            assert e.value.status == 1
+    c.check(sm_scale=2.0 ** -126)
