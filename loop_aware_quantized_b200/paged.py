@@ -296,7 +296,7 @@ def paged_decode(cells, q, k_pages, v_pages, table, lengths, meta=None, cur_k=No
     if (cur_k is None) != (cur_v is None):
         raise _invalid(where, "cur_k and cur_v come together")
     if current is not None:
-        flags = np.ascontiguousarray(current, dtype=np.uint8).reshape(-1)
+        flags = np.asarray(current).astype(bool).reshape(-1)  # (not by way of 8 bits: 256 is true)
         if flags.size != n_cells:
             raise _invalid(where, "current must hold %d values, not %d" % (n_cells, flags.size))
         if cur_k is None and flags.any():

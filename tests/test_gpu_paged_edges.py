@@ -254,3 +254,14 @@ def test_positive_scales_that_fp32_loses_are_refused(dev):
                 paged_decode([0], c.q, c.kp, c.vp, t, n, sm_scale=scale, stream=stream)
             assert e.value.status == 1
     c.check(sm_scale=2.0 ** -126)
+
+
+def test_flags_are_truth_values(dev):
+    import torch
+    from loop_aware_quantized_b200 import paged_decode
+    c = Case(dev, "bf16", [10, 20], heads=2, group=2, dim=64, cells=(0, 0, 0, 0), seed=62)
+    args = (c.cells, c.q, c.kp, c.vp, ints(c.table, dev), ints(c.lengths, dev))
+    want = paged_decode(*args, cur_k=c.cur[0], cur_v=c.cur[1], current=[True, False, True, True])
+    assert (want[0] != want[1]).any()
+    for flags in (np.array([256, 0, 512, -256]), [256, 0, 2 ** 40, 0.25], np.array([0.5, 0.0, 1e-9, -1.0])):
+        assert (paged_decode(*args, cur_k=c.cur[0], cur_v=c.cur[1], current=flags) == want).all()
