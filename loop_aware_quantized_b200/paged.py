@@ -215,9 +215,29 @@ def _rows(t, where, name, dtype, index, shape):
     return _lk.loopkv_rows(at, cell, row, head)
 
 
+def _to_int32(given, where):
+    """The numbers as int32, none of them changed by it (2^32 is not cell 0)."""
+    try:
+        if given.dtype.kind in "iu":
+            a = given.astype(np.int32)
+            same = a.astype(given.dtype).tobytes() == given.tobytes()  # (a third of the time of a comparison)
+        else:
+            with np.errstate(invalid="ignore"):
+                a = given.astype(np.int32)
+            same = bool((a == given).all())
+    except (TypeError, ValueError, OverflowError):
+        same = False
+    if not same:
+        raise _invalid(where, "cells must be numbers of cells, not %r" % (given,))
+    return a
+
+
 def _cells(cells, where):
     """Host int32 array of a list of cells."""
-    a = np.ascontiguousarray(cells, dtype=np.int32).reshape(-1)
+    a = np.asarray(cells)
+    if a.dtype != np.int32:
+        a = _to_int32(a, where)
+    a = np.ascontiguousarray(a).reshape(-1)
     if not 1 <= a.size <= _lk.LOOPKV_MAX_CELLS_PER_CALL:
         raise _invalid(where, "1 to %d cells in a call, not %d" % (
             _lk.LOOPKV_MAX_CELLS_PER_CALL, a.size))

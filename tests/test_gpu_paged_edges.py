@@ -265,3 +265,61 @@ def test_flags_are_truth_values(dev):
     assert (want[0] != want[1]).any()
     for flags in (np.array([256, 0, 512, -256]), [256, 0, 2 ** 40, 0.25], np.array([0.5, 0.0, 1e-9, -1.0])):
         assert (paged_decode(*args, cur_k=c.cur[0], cur_v=c.cur[1], current=flags) == want).all()
+
+
+def test_what_one_way_refuses_the_other_does(dev):
+    # the compiled checks (the current stream) and those in Python (a stream given): every bad
+    # argument fails on both, and the first way leaves it to the second or names the same error
+    import torch
+    from loop_aware_quantized_b200 import _paged, page_map, page_release, paged_append, paged_decode
+    from loop_aware_quantized_b200.loopkv import LoopKVError
+    c = Case(dev, "q8", [10, 20], heads=2, group=2, dim=64, seed=63)
+    t, n = ints(c.table, dev), ints(c.lengths, dev)
+    i2, one, s2 = ints([1, 1], dev), ints([2], dev), ints([1, 2], dev)
+    free = ints(np.arange(c.shape[1]), dev)
+    wide = torch.zeros((1, 2, 2, 68), dtype=torch.bfloat16, device=dev)
+    vec, vec4 = c.cur[0], c.q
+    calls = {
+        "page_map": (page_map, dict(lengths=n, n_new=i2, table=t, free=free, free_count=one, page_size=16, slots=s2,
+                                    starts=ints([0] * 3, dev), newest=None, lengths_out=None, free_count_out=None, status=None)),
+        "page_release": (page_release, dict(lengths=n, new_lengths=n.clone(), table=t, free=free, free_count=one, page_size=16,
+                                            lengths_out=None, free_count_out=None, status=None)),
+        "paged_append": (paged_append, dict(cells=[0], k=vec, v=vec, slots=s2, k_pages=c.kp, v_pages=c.vp, meta=c.meta,
+                                            status=None)),
+        "paged_decode": (paged_decode, dict(cells=[0], q=vec4, k_pages=c.kp, v_pages=c.vp, table=t, lengths=n, meta=c.meta,
+                                            cur_k=None, cur_v=None, current=None, out=None, lse=None, sm_scale=0.0,
+                                            status=None)),
+    }
+    ints_bad = [n.long(), n.float(), n[:1], n.cpu(), ints([0] * 4, dev)[::2], ints([0] * 3, dev), t]
+    vec_bad = [vec.half(), vec.float(), vec[..., :32], vec[:, :1], wide[..., 2:66], wide[..., :64], vec[0], vec.cpu()]
+    pages_bad = [c.kp.to(torch.int32), c.kp[0], c.kp[..., :32], c.kp[:, :0], c.kp.cpu(), c.kp.transpose(1, 2)]
+    bad = {
+        "lengths": ints_bad, "n_new": ints_bad, "new_lengths": ints_bad, "lengths_out": ints_bad, "newest": ints_bad,
+        "table": [t.long(), t.t(), t[0], t[:1], t[:, :0], t.cpu()], "free": [free.long(), t, free.cpu(), free[:0]],
+        "free_count": [i2, one.long(), one.cpu()], "free_count_out": [i2, one.long(), one.cpu()],
+        "status": [i2, one.long(), one.cpu()], "starts": [n, ints([0] * 4, dev), ints([0] * 3, dev).long()],
+        "page_size": [0, -1, 1025, 16.5, True, 1 << 40], "k": vec_bad, "v": vec_bad, "cur_k": vec_bad + [vec], "cur_v": vec_bad + [vec],
+        "q": [vec4.half(), vec4[..., :32], vec4[:, :1], vec4[:, :, :3], vec4.cpu(), wide[..., 2:66]],
+        "k_pages": pages_bad, "v_pages": pages_bad, "meta": [None, c.meta.half(), c.meta[..., :3], c.meta.cpu()],
+        "cells": [[], [1], [-2], [0, 0], [2 ** 32], list(range(300)), np.array([2 ** 32]), np.array([[0.5]])],
+        "current": [[True], np.array([1], np.uint8), [True, False]], "out": [vec4.float(), vec4[:, :, :2], vec4.cpu(), vec4.half()],
+        "lse": [torch.zeros(3, device=dev), torch.zeros((1, 2, 4), device=dev).double()],
+        "sm_scale": [float("nan"), float("inf"), 1e300, 1e20],
+        "slots": [s2.long(), s2.cpu(), t],
+    }
+    before = [x.clone() for x in (c.kp, c.vp, t, n, free, one)]
+    tried = 0
+    for name, (fn, good) in calls.items():
+        short = getattr(_paged, name)
+        for arg in good:
+            for x in bad[arg]:
+                kw = {**good, arg: x}
+                got = short(*kw.values())
+                assert got in (-1, 1), (name, arg, x)
+                for stream in (None, torch.cuda.current_stream()):
+                    with pytest.raises(LoopKVError) as e:
+                        fn(**kw, stream=stream)
+                    assert e.value.status == 1, (name, arg, x)
+                tried += 1
+    torch.cuda.synchronize()
+    assert tried > 150 and all((a == b).all() for a, b in zip(before, (c.kp, c.vp, t, n, free, one)))
