@@ -55,7 +55,7 @@ def paged_decode_step(cache, phase_cells, ones, slots, q, k_new, v_new, out, lse
     cache.grow(ones, slots, stream=stream)
     for i, cells in enumerate(phase_cells):
         cache.append(cells, k_new[i], v_new[i], cache.newest, stream=stream)
-        shares = cache.shared[cells].any()
+        shares = cache.shared[np.asarray(cells)].any()  # (a tuple would be an index per axis)
         cache.decode(cells, q[i], cur_k=k_new[i] if shares else None,
                      cur_v=v_new[i] if shares else None, out=out[i],
                      lse=None if lse is None else lse[i], stream=stream)

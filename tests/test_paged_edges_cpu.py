@@ -26,3 +26,27 @@ def test_cells_that_32_bits_lose_are_refused(lk):
     for cells in (range(2), (0, 1), [np.int64(1)], np.array([0.0, 1.0]), np.array([[0, 1]], np.uint8)):
         with pytest.raises(lk.LoopKVError, match="k_pages must"):    # the next argument's turn
             cache.append(cells, None, None, None)
+
+
+def test_step_takes_any_form_of_a_phase(lk):
+    # tuples of cells, as append and decode take them, and the current tokens where a cell shares
+    from loop_aware_quantized_b200 import steps
+
+    class Cache:
+        shared, newest, calls = np.array([True, False, False, False]), "newest", []
+
+        def grow(self, ones, slots, stream=None):
+            self.calls.append(("grow", ones))
+
+        def append(self, cells, k, v, slots, stream=None):
+            self.calls.append(("append", list(cells), k, slots))
+
+        def decode(self, cells, q, cur_k=None, cur_v=None, out=None, lse=None, stream=None):
+            self.calls.append(("decode", list(cells), cur_k))
+
+    for forms in (((0, 1), (2, 3)), ([0, 1], [2, 3]), (range(2), range(2, 4)), (np.arange(2), np.arange(2, 4))):
+        cache = Cache()
+        cache.calls = []
+        steps.paged_decode_step(cache, forms, "ones", "slots", "qq", "kK", "vV", ["o", "p"])
+        assert cache.calls == [("grow", "ones"), ("append", [0, 1], "k", "newest"), ("decode", [0, 1], "k"),
+                               ("append", [2, 3], "K", "newest"), ("decode", [2, 3], None)]
