@@ -323,3 +323,53 @@ def test_what_one_way_refuses_the_other_does(dev):
                 tried += 1
     torch.cuda.synchronize()
     assert tried > 150 and all((a == b).all() for a, b in zip(before, (c.kp, c.vp, t, n, free, one)))
+
+
+# -------------------------------------------------------------- many blocks
+
+def test_page_map_refuses_on_many_blocks(dev):
+    # refused requests of every kind among admitted ones, rows just above what one block takes
+    ps, width = 8, 40
+    for rows, batch in ((256, 60), (257, 60), (3000, 60), (9000, 700), (9000, 2500)):
+        rng = np.random.default_rng(rows + batch)
+        lengths = rng.integers(0, 100, batch)
+        new = np.bincount(rng.integers(0, batch, rows), minlength=batch)
+        table, free, count = make_tables(rng, lengths, width, ps, batch * width)
+        lengths[3], new[7], lengths[11], new[20] = -5, -2, 2 ** 31 - 1, 2 ** 31 - 1
+        table[1, :13] = batch * width                    # held pages outside the pool
+        free[count - 3:count - 1] = -1
+        need = int(np.maximum(0, new[:18]).sum()) // ps + 20
+        for in_place in (False, True):
+            st = check_map(dev, lengths, new, table, free, count, ps, rows, in_place)[5]
+            assert st & R.BAD_LENGTH and st & R.NO_TABLE and st & R.NO_ROWS
+            check_map(dev, lengths, np.minimum(new, 500), table, free, min(need, count), ps, rows + 1000, in_place)
+
+
+@pytest.mark.parametrize("n_pages", [255, 256, 257, 4095, 4096, 4097, 20000])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_page_release_refuses_on_any_number_of_blocks(dev, n_pages, in_place):
+    # one block takes 256 pages, in place 4096: bad lengths, bad entries, a list that is nearly full
+    from loop_aware_quantized_b200 import page_release
+    rng = np.random.default_rng(n_pages)
+    batch = 40
+    width = -(-n_pages // batch) + 1
+    lengths = rng.integers(0, n_pages // batch + 1, batch)
+    table, free, count = make_tables(rng, lengths, width, 1, n_pages)
+    new = np.where(rng.random(batch) < 0.8, 0, lengths // 2)
+    for case in ("plain", "bad", "nearly full", "full"):
+        n, a, tab, cnt = lengths.copy(), new.copy(), table.copy(), count
+        if case != "plain":
+            n[2], a[5], a[9], n[13] = -1, -1, n[9] + 1, width + 1
+            tab[20, :n[20]] = n_pages
+            tab[21, :n[21] // 2] = -9
+        if case == "nearly full":
+            cnt = n_pages - int((n[:12] - a[:12]).clip(0).sum()) - 1
+        if case == "full":
+            cnt = n_pages
+        t = [ints(x, dev) for x in (n, a, tab, free, [cnt])]
+        lo, co = (t[0], t[4]) if in_place else (ints(np.full(batch, 99), dev), ints([99], dev))
+        status = ints([0], dev)
+        page_release(*t, 1, lengths_out=None if in_place else lo, free_count_out=None if in_place else co, status=status)
+        f, out, c, st = R.page_release(n, a, tab, free, cnt, 1)
+        assert np.array_equal(host(t[3]), f) and np.array_equal(host(lo), out) and int(co) == c and int(status) == st, case
+        assert np.array_equal(host(t[2]), tab)
