@@ -1632,12 +1632,22 @@ constexpr size_t decode_smem(int S) {
                           (size_t)G * S);
 }
 
+// Largest score slots per query that keep two CTAs on an SM (at most
+// kMaxSlots in all), for a group of G queries.
+template <int D, int G>
+constexpr int max_slots_g() {
+  constexpr size_t kBudget = 113 * 1024;  // bytes of shared memory per CTA for two CTAs per SM
+  constexpr size_t fixed = decode_smem<D, G>(0);
+  constexpr size_t per_query = (kBudget - fixed) / sizeof(float);  // G * S + S / 32 <= this
+  constexpr size_t s = per_query * 32 / (32 * G + 1) / 32 * 32;
+  return (int)(s * G > (size_t)kMaxSlots ? kMaxSlots / G : s);
+}
+
 template <int D, int G, bool DENSE_LO, bool RES2>
 int launch_decode_t(const DecodeParams& p, const CellList& cells, cudaStream_t stream) {
   const size_t smem = decode_smem<D, G>(p.slots);
-  cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, G, DENSE_LO, RES2>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return (int)e;
+  if (!allow_shared(decode_kernel<D, G, DENSE_LO, RES2>, decode_smem<D, G>(max_slots_g<D, G>())))
+    return (int)cudaErrorInvalidValue;
   const long long units = (long long)p.n_cells * p.batch * p.n_heads;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(units * p.split), 1, 1);
@@ -1655,8 +1665,7 @@ int launch_decode_t(const DecodeParams& p, const CellList& cells, cudaStream_t s
   }
   cfg.attrs = attr;
   cfg.numAttrs = nattr;
-  e = cudaLaunchKernelEx(&cfg, decode_kernel<D, G, DENSE_LO, RES2>, p, cells);
-  return (int)e;
+  return (int)cudaLaunchKernelEx(&cfg, decode_kernel<D, G, DENSE_LO, RES2>, p, cells);
 }
 
 template <int D, int G, bool RES2>
@@ -1671,17 +1680,6 @@ int launch_decode_d(const DecodeParams& p, const CellList& cells, cudaStream_t s
   if (p.group == 2) return launch_decode_g<D, 2, RES2>(p, cells, s);
   if (p.group == 4) return launch_decode_g<D, 4, RES2>(p, cells, s);
   return launch_decode_g<D, 1, RES2>(p, cells, s);
-}
-
-// Largest score slots per query that keep two CTAs on an SM (at most
-// kMaxSlots in all), for a group of G queries.
-template <int D, int G>
-constexpr int max_slots_g() {
-  constexpr size_t kBudget = 113 * 1024;  // bytes of shared memory per CTA for two CTAs per SM
-  constexpr size_t fixed = decode_smem<D, G>(0);
-  constexpr size_t per_query = (kBudget - fixed) / sizeof(float);  // G * S + S / 32 <= this
-  constexpr size_t s = per_query * 32 / (32 * G + 1) / 32 * 32;
-  return (int)(s * G > (size_t)kMaxSlots ? kMaxSlots / G : s);
 }
 
 }  // namespace

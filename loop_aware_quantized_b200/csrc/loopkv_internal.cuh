@@ -186,8 +186,8 @@ __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontr
 
 // Dynamic shared memory that any call of a kernel may ask for.  The limit belongs to
 // the function and the device, not to the call, so it is the same for every call:
-// one that followed the batch could be lowered by another thread between a call's
-// setting and its launch, which then fails.
+// one that followed a call's sizes could be lowered by another thread between the
+// call's setting and its launch, which then fails.
 template <typename... P>
 bool allow_shared(void (*kernel)(P...), size_t most) {
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) == cudaSuccess) return true;
