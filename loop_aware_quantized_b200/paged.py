@@ -147,7 +147,7 @@ def page_map(lengths, n_new, table, free, free_count, page_size, slots, starts, 
     d_count_out = d_count if free_count_out is None else _ints(free_count_out, where, "free_count_out", index, one)
     d_status = None if status is None else _ints(status, where, "status", index, one)
     handle, context = _place(where, index, stream)
-    _launch(_lk._lib.loopkv_page_map, context, batch, page_size, width, n_pages, rows, d_len, d_new, d_table,
+    _launch(_lk.loopkv_page_map, context, batch, page_size, width, n_pages, rows, d_len, d_new, d_table,
             d_free, d_count, d_slots, d_starts, d_newest, d_len_out, d_count_out, d_status, handle)
     return slots, starts
 
@@ -180,7 +180,7 @@ def page_release(lengths, new_lengths, table, free, free_count, page_size, lengt
     d_count_out = d_count if free_count_out is None else _ints(free_count_out, where, "free_count_out", index, one)
     d_status = None if status is None else _ints(status, where, "status", index, one)
     handle, context = _place(where, index, stream)
-    _launch(_lk._lib.loopkv_page_release, context, batch, page_size, width, n_pages, d_len, d_new, d_table, d_free,
+    _launch(_lk.loopkv_page_release, context, batch, page_size, width, n_pages, d_len, d_new, d_table, d_free,
             d_count, d_len_out, d_count_out, d_status, handle)
 
 
@@ -265,8 +265,7 @@ def paged_append(cells, k, v, slots, k_pages, v_pages, meta=None, status=None, s
     d_slots = _ints(slots, where, "slots", index, (rows,))
     d_status = None if status is None else _ints(status, where, "status", index, (1,))
     handle, context = _place(where, index, stream)
-    _launch(_lk._lib.loopkv_paged_append, context, ctypes.addressof(pool), cells.tobytes(), cells.size, rows,
-            d_slots, ctypes.addressof(kr), ctypes.addressof(vr), d_status, handle)
+    _launch(_lk.loopkv_paged_append, context, pool, cells.tobytes(), cells.size, rows, d_slots, kr, vr, d_status, handle)
 
 
 @functools.lru_cache(maxsize=256)
@@ -340,11 +339,9 @@ def paged_decode(cells, q, k_pages, v_pages, table, lengths, meta=None, cur_k=No
     def launch():  # memory made here belongs to the stream of the launch
         work = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
         got = torch.empty(q.shape, dtype=dtype, device=q.device) if out is None else out
-        rc = _lk._lib.loopkv_paged_decode(
-            ctypes.addressof(pool), ctypes.addressof(desc), cells.tobytes(), flags, n_cells, d_table, d_len,
-            ctypes.addressof(qr), None if kr is None else ctypes.addressof(kr),
-            None if vr is None else ctypes.addressof(vr), got.data_ptr() if d_out is None else d_out, d_lse,
-            work.data_ptr(), nbytes, d_status, handle)
+        rc = _lk.loopkv_paged_decode(
+            pool, desc, cells.tobytes(), flags, n_cells, d_table, d_len, qr, kr, vr,
+            got.data_ptr() if d_out is None else d_out, d_lse, work.data_ptr(), nbytes, d_status, handle)
         if rc:
             _check(rc, "loopkv_paged_decode")
         return got
