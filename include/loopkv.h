@@ -549,7 +549,8 @@ loopkv_status loopkv_paged_workspace(const loopkv_page_pool* pool, const loopkv_
  * weights up to 2^8: 16-bit values above 2^98 may overflow them.  For Q8,
  * queries lie below 2^64 in magnitude (they meet the codes times 2^64 in bf16;
  * larger ones give NaN or infinity) and scales of values below 2^56
- * (LOOPKV_PAGE_BAD_VALUE).  The order of all sums is fixed by the sizes and
+ * (LOOPKV_PAGE_BAD_VALUE).  Scores lie below 2^24 in magnitude, where fp32
+ * still holds whole numbers.  The order of all sums is fixed by the sizes and
  * lengths.
  * Errors (nothing launched): LOOPKV_ERR_INVALID_ARG (null or misaligned
  * pointers, sizes, a workspace below loopkv_paged_workspace's bytes),

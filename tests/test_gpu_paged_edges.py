@@ -373,3 +373,73 @@ def test_page_release_refuses_on_any_number_of_blocks(dev, n_pages, in_place):
         f, out, c, st = R.page_release(n, a, tab, free, cnt, 1)
         assert np.array_equal(host(t[3]), f) and np.array_equal(host(lo), out) and int(co) == c and int(status) == st, case
         assert np.array_equal(host(t[2]), tab)
+
+
+# ------------------------------------------------------------ largest sizes
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp16", "q8"])
+def test_decode_of_the_largest_scores(dev, fmt):
+    # scores of 2^23 and -2^23, exact in fp32: the one above the others by 2^10 takes all the weight,
+    # equal ones share it
+    import torch
+    for sign in (1, -1):
+        c = Case(dev, fmt, [48, 16, 1], heads=2, group=2, dim=64, ps=16, seed=70, width=3)
+        c.q.fill_(2.0 ** 11)
+        if fmt == "q8":
+            c.kp.fill_(128)
+            c.meta[..., 0], c.meta[..., 1] = sign * 2.0 ** 4, 0
+        else:
+            c.kp.fill_(sign * 2.0 ** 11)
+        # <q, k> = 64 * 2^11 * 2^11 = 2^28; the first request's token 20 has 64 * 2^11 * 8 = 2^20 more
+        page = int(c.table[0, 1])
+        if fmt == "q8":
+            c.meta[0, page, :, 4, 1] += 8.0
+        else:
+            c.kp[0, page, :, 4] += 2.0 ** 3 if fmt == "fp16" else 2.0 ** 4  # (a step of bf16 is 8 below, 16 above 2^11)
+        out, lse, status = c.run(sm_scale=2.0 ** -5)
+        o, e = host(out).astype(np.float64)[0], host(lse)[0]
+        v, size = R.stored(host(c.vp), None if c.meta is None else host(c.meta), 2)
+        for b, n in enumerate(c.lengths):
+            pos = np.arange(n) if b else np.array([20])
+            want, around = (x[0, c.table[b, pos // 16], :, pos % 16].mean(0).repeat(2, 0) for x in (v, size))
+            # weights to 2^-16, twice over with their sum, and the output's rounding
+            assert (np.abs(o[b] - want) <= 2.0 ** -14 * around + (2.0 ** -11 if fmt == "fp16" else 2.0 ** -8) * np.abs(want)).all()
+        assert status == 0 and (np.abs(np.abs(e) - 2.0 ** 23) <= 2.0 ** 17).all()
+
+
+def test_decode_of_the_most_heads_and_cells(dev):
+    # 65536 heads of one request; 256 listed cells, apart and shared
+    import torch
+    from loop_aware_quantized_b200 import paged_append, paged_decode
+    heads = 1 << 16
+    g = torch.Generator(device=dev).manual_seed(71)
+    k, v, q = (torch.randn((1, 2, heads, 64), generator=g, device=dev).to(torch.bfloat16) for _ in range(3))
+    kp, vp = (torch.zeros((1, 3, heads, 1, 64), dtype=torch.bfloat16, device=dev) for _ in range(2))
+    paged_append([0], k, v, ints([2, 0], dev), kp, vp)
+    out = paged_decode([0], q, kp, vp, ints([[2], [0]], dev), ints([1, 1], dev))
+    assert (out == v).all()                              # one token each: its value
+    cells = 256
+    k, v, q = (torch.randn((cells, 2, 3, 64), generator=g, device=dev).to(torch.bfloat16) for _ in range(3))
+    kp, vp = (torch.zeros((cells, 3, 3, 1, 64), dtype=torch.bfloat16, device=dev) for _ in range(2))
+    order = np.random.default_rng(0).permutation(cells)
+    paged_append(order, k, v, ints([2, 0], dev), kp, vp)
+    t, n = ints([[2], [0]], dev), ints([1, 1], dev)
+    assert (paged_decode(order, q, kp, vp, t, n) == v).all()
+    at = int(order[5])
+    assert (paged_decode([at] * cells, q, kp, vp, t, n) == v[5]).all()
+    assert (paged_decode([at] * cells, q, kp, vp, t, n, cur_k=k, cur_v=v) == v).all()
+
+
+@pytest.mark.parametrize("fmt,dim,group", [("bf16", 64, 1), ("fp16", 64, 4), ("q8", 128, 8), ("bf16", 128, 16)])
+def test_decode_repeats_itself_bit_for_bit(dev, fmt, dim, group):
+    # split units, their joins, other work on the GPU between: the order of sums does not change
+    import torch
+    c = Case(dev, fmt, [50000, 3, 0, 700, 7001], heads=2, group=group, dim=dim, ps=16, seed=72)
+    first = c.run()
+    side, x = torch.cuda.Stream(dev), torch.randn((2048, 2048), device=dev)
+    for i in range(20):
+        if i % 2:
+            with torch.cuda.stream(side):
+                x = torch.tanh(x @ x)
+        again = c.run()
+        assert (first[0] == again[0]).all() and (first[1] == again[1]).all()
