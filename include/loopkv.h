@@ -442,7 +442,8 @@ typedef enum {
  * count is negative (BAD_LENGTH), when it would outgrow max_pages (NO_TABLE)
  * or its rows end behind n_rows (NO_ROWS), and, needing pages, when they and
  * those of the requests before it (refused ones not counted but for this
- * reason) are more than the free list has (NO_PAGES).  A page id outside
+ * reason) are more than the free list has (NO_PAGES).  A free count outside 0
+ * .. n_pages counts as 0 (BAD_LENGTH).  A page id outside
  * 0 .. n_pages-1 gives slots -1 (BAD_PAGE).  d_free: int32 [n_pages], of which
  * the first *d_free_count are free pages.  d_len_out may be d_len and
  * d_free_count_out may be d_free_count (d_len_out equal to d_new is refused).

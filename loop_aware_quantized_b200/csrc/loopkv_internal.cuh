@@ -177,8 +177,8 @@ struct PageDiv {
 // predecessor's end and writes before it reads or writes anything (one
 // exception: page_map's and page_release's finishing launch).  A kernel that has
 // ended has waited, so its successor is behind all that came before it too.
-// Calls one after another: a page map 6.2 -> 3.8 us, one request's decode 16.5 ->
-// 13.  Letting the successor start with the predecessor's first blocks
+// Calls one after another, when this came: a page map 6.2 -> 3.8 us, one request's
+// decode 16.5 -> 13.  Letting the successor start with the predecessor's first blocks
 // (let_next_launch) pays only where it has work to do before it waits: its blocks
 // take places unevenly, and 67 ragged requests' decode took 94 us instead of 83.
 __device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

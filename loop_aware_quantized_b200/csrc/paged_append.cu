@@ -8,9 +8,10 @@
 // (Q8: four such pieces of each, a quarter vector apart); a vector's threads sit
 // in one warp, so its minimum and maximum are a few shuffles.  What bounds it:
 // memory.  Each byte is read once and written once; a vector is 128 or 256
-// contiguous bytes on both sides.  36000 rows of 16 heads of 128 in fp16: 94 us, 6.27
+// contiguous bytes on both sides.  36000 rows of 16 heads of 128 in fp16: 96 us, 6.1
 // TB/s.  With a division per value Q8 took more than twice as long as its bytes
-// (2 cells of 16384 rows: 175 us, now 65): see codes8.
+// (2 cells of 16384 rows: 175 us, 68 now; 75 where the runs are seconds long and the
+// power cap lowers the clock): see codes8.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -26,8 +27,8 @@ namespace {
 constexpr int kThreads = 128;
 // 16-byte pieces of a key vector and of a value vector that a Q8 thread does:
 // what is done once per vector (scale, reciprocal, addresses) is shared by so
-// many more values (2: 78 us, 4: 65 us of 63 that the bytes take; 2 cells of 16384 rows,
-// 16 heads of 128).
+// many more values (2: 78 us, 4: 65 us of 63 that the bytes take, short runs; 2 cells of
+// 16384 rows, 16 heads of 128).
 constexpr int kPieces = 4;
 
 struct PagedAppendParams {

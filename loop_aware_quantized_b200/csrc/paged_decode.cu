@@ -18,15 +18,17 @@
 // replaced while its values are still used.  Rows behind a request's length
 // and rows of bad pages are filled with zeros and not read.  Direct loads into
 // registers, 12 warps to an SM as here, waited for a tile at a time: 781 us
-// instead of 615 for 32 requests of 16384 tokens, 200 instead of 82 for 67 ragged ones.
+// instead of 615 for 32 requests of 16384 tokens, 200 instead of 82 for 67 ragged ones
+// (short runs, in turn).
 //
-// Measured (bytes of the pages over the time, both kernels): 32 requests of
-// 16384 tokens, 16 heads of 128 in bf16 615 us, 7.0 TB/s; 67 ragged requests of
-// 120000 tokens in 2 cells, 8 heads of 64 with 4 queries in fp16 82 us, 6.0
-// TB/s; at 1 GB pages of 1 token 6.4 TB/s, of 24 tokens 6.2, 8 bits a value 5.7 to
-// 6.1 with 1 and 8 queries and 5.3 with 16, where the conversion of codes (a
-// byte permute per two) takes the issue slots.  Small calls: one request of
-// 4113 tokens, 33.7 MB, 11 us, of which the join's launch and round trips are 3.
+// Measured (bytes of the pages over the time, both kernels).  Seconds long, under
+// the power cap: 32 requests of 16384 tokens, 16 heads of 128 in bf16 631 us, 6.8
+// TB/s; 67 ragged requests of 120000 tokens in 2 cells, 8 heads of 64 with 4
+// queries in fp16 84 us, 5.9 TB/s; one request of 4113 tokens, 33.7 MB, 11 us, of
+// which the join's launch and round trips are 3.  Short runs on 1 GB: pages of 1
+// token 6.5 TB/s, of 24 tokens 6.2, 8 bits a value 5.9 to 6.1 with 1 and 8 queries and
+// 5.4 to 5.6 with 16, where the conversion of codes (a byte permute per two) takes
+// the issue slots.
 // mma.sync and not tcgen05: a tile of 128 rows would be seven eighths padding and
 // its results a trip to tensor memory away, and the tensor pipe is 5 to 20 % busy.
 //
@@ -82,7 +84,7 @@ constexpr int kSms = 148;
 constexpr int kMaxWorkers = kSms * 3;
 constexpr int kPage = 16;             // pages of a multiple of this are FLAT (below)
 constexpr int kMinTokens = 128;       // what a worker takes at least
-constexpr int kUnitTokens = 384;      // tokens that a unit's start and end are worth
+constexpr int kUnitTokens = 384;      // tokens that a unit's start and end are worth (the largest tried)
 constexpr int kEmptyTokens = 32;      // and a unit without tokens, which is only written
 constexpr int kMaxRows = LOOPKV_MAX_PAGED_GROUP;  // query rows of a set
 constexpr int kJoinThreads = 256;
@@ -271,8 +273,8 @@ struct Shape {
   static __device__ __forceinline__ int swizzle(int t) { return kPieces == 4 ? (t >> 1) & 3 : t & 7; }
 };
 
-// MODE 0: up to 4 query rows, 1: 8, 2: 16.  FLAT: pages of whole tiles, so that
-// a tile's rows follow one another.
+// MODE 0: up to 4 query rows, 1: 8, 2: 16.  FLAT: pages of whole runs of 16 tokens,
+// so that the rows of a tile, or of each half of one of 32, follow one another.
 template <int D, int FMT, int MODE, bool FLAT>
 __global__ void __launch_bounds__(kThreads, Shape<D, FMT, MODE>::kCtasPerSm)
 paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_constant__ Sets sets) {

@@ -14,12 +14,14 @@
 // and free count.  Where these take the old ones' place, nothing may read the
 // old ones any more: a short call is one CTA and a block barrier; a long one is a
 // grid that expands, and one more CTA, launched while the grid runs, that
-// repeats the prefix sum, waits for the grid's end and stores (a million rows:
-// 9.1 us, 8.5 where the outputs lie elsewhere and the grid does it all).  So
-// lengths are updated in place, and a call can be captured and replayed.  What
-// bounds it: the launch and two dependent memory round trips (lengths, then
-// free list or table); 32 requests' step takes 3.6 us, releases of a small batch
-// 3.5, half a million pages given back 6.7.
+// repeats the prefix sum, waits for the grid's end and stores (a million rows
+// brought and cut again: 13.9 us a pair, 12.1 where the outputs lie elsewhere and
+// the grid does it all).  So lengths are updated in place, and a call can be
+// captured and replayed.  What bounds it: a short call, the launch and two
+// dependent memory round trips (lengths, then free list or table), 3.4 us for 32
+// requests' step and 3.1 for the release of a small batch; a long one, instructions
+// (67 and 54 % of the issue slots: a search, a division and an address per row or
+// page), 8.2 us for a million rows and 6.6 for half a million pages given back.
 
 #include <cuda_runtime.h>
 
@@ -321,7 +323,7 @@ page_release_kernel(const __grid_constant__ PageParams p) {
   for (int k = 0; k < kPerThread; ++k) {
     const int b = tid * per + k;
     if (k >= per || b >= p.batch) continue;
-    // starts of refused requests lie at or behind `room`, where no push is made
+    // refused requests start at or behind the pages pushed, where no push is made
     sh.start[b] = (int)(before < room ? before : room);
     sh.a[b] = gone[k] > 0 ? p.div.pages(cut[k]) : 0;
     before += gone[k];
