@@ -374,7 +374,10 @@ class PagedCache:
         self.n_loops, self.n_layers, self.n_cells = n_loops, n_layers, n_loops * n_layers
         self.page_size, self.sm_scale = page_size, float(sm_scale)
         self.shared = np.zeros(self.n_cells, bool)
-        for cell in shared:
+        shared = np.asarray(list(shared))
+        if shared.dtype.kind == "b":
+            raise _invalid(where, "shared must be a list of cells, not of truth values")
+        for cell in _to_int32(shared, where):
             if not 0 <= cell < self.n_cells - n_layers:
                 raise _invalid(where, "cell %d cannot share: only cells of non-final loops" % cell)
             self.shared[cell] = True

@@ -50,3 +50,16 @@ def test_step_takes_any_form_of_a_phase(lk):
         steps.paged_decode_step(cache, forms, "ones", "slots", "qq", "kK", "vV", ["o", "p"])
         assert cache.calls == [("grow", "ones"), ("append", [0, 1], "k", "newest"), ("decode", [0, 1], "k"),
                                ("append", [2, 3], "K", "newest"), ("decode", [2, 3], None)]
+
+
+def test_shared_is_a_list_of_cells_not_a_mask(lk):
+    # (as an index, a truth value would mark every cell or none)
+    from loop_aware_quantized_b200 import PagedCache
+    make = lambda shared: PagedCache(2, 2, 1, 64, 4, 16, 2, 4, shared=shared, device="cpu")  # noqa: E731
+    for shared in (np.array([True, False, False, False]), [False, True], [True], [0.5], np.array([1 << 32]), ["x"]):
+        with pytest.raises(lk.LoopKVError) as e:
+            make(shared)
+        assert e.value.status == 1
+    for shared in ([1], (1,), range(1, 2), np.array([1]), {1}, np.array([1.0]), iter([1])):
+        assert make(shared).shared.tolist() == [False, True, False, False]
+    assert not make(()).shared.any() and not make(np.array([], np.int32)).shared.any()
